@@ -45,6 +45,33 @@ class Csr(ctypes.Structure):
                 ("nnz", ctypes.c_void_p), ("status", ctypes.c_void_p), ("col_code", ctypes.c_void_p)]
 
 
+class Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("s", ctypes.c_int64)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("S", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64),
+                ("d", ctypes.c_int64), ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("table_rows", ctypes.c_int64), ("q", Strides), ("k", Strides), ("qo", Strides), ("ko", Strides),
+                ("dq", Strides), ("dk", Strides)]
+
+
+class DenseShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("Sq", ctypes.c_int64),
+                ("Sk", ctypes.c_int64), ("d", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("causal", ctypes.c_int32), ("q", Strides), ("k", Strides),
+                ("v", Strides), ("o", Strides), ("dout", Strides), ("dq", Strides), ("dk", Strides), ("dv", Strides)]
+
+
+class DenseMask(ctypes.Structure):
+    _fields_ = [("slopes", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p), ("doc_q", ctypes.c_void_p), ("doc_k", ctypes.c_void_p)]
+
+
+SIZE_ERROR = ctypes.c_size_t(-1).value       # a size call's answer to invalid arguments
+
+
 class FvattnError(RuntimeError):
     def __init__(self, code: int, what: str):
         msg = f"{what}: {status_string(code)} ({code})"
@@ -126,6 +153,22 @@ def load() -> ctypes.CDLL:
                                     ctypes.c_int64, P(ctypes.c_int32), vp]
     lib.fvattn_select_heads.restype = ctypes.c_int
     lib.fvattn_select_heads.argtypes = [P(Shape), P(Csr), vp, vp]
+    lib.fvattn_qk_norm_rope.restype = ctypes.c_int
+    lib.fvattn_qk_norm_rope.argtypes = [vp, vp, P(QkShape), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.fvattn_qk_norm_rope_workspace_bytes.restype = ctypes.c_size_t
+    lib.fvattn_qk_norm_rope_workspace_bytes.argtypes = [P(QkShape)]
+    lib.fvattn_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.fvattn_qk_norm_rope_bwd.argtypes = [vp, vp, vp, vp, P(QkShape), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                            ctypes.c_size_t, vp, vp]
+    lib.fvattn_dense_attn_workspace_bytes.restype = ctypes.c_size_t
+    lib.fvattn_dense_attn_workspace_bytes.argtypes = [P(DenseShape), P(DenseMask)]
+    lib.fvattn_dense_attn.restype = ctypes.c_int
+    lib.fvattn_dense_attn.argtypes = [vp, vp, vp, P(DenseShape), P(DenseMask), vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
+    lib.fvattn_dense_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.fvattn_dense_attn_bwd_workspace_bytes.argtypes = [P(DenseShape), P(DenseMask)]
+    lib.fvattn_dense_attn_bwd.restype = ctypes.c_int
+    lib.fvattn_dense_attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, P(DenseShape), P(DenseMask), vp, vp, vp, vp,
+                                          ctypes.c_size_t, vp, vp]
     _lib = lib
     return lib
 

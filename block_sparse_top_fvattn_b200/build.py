@@ -25,8 +25,10 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfvattn.so")
 DEBUG_LIB = os.path.join(PKG, "libfvattn_debug.so")
 
-SOURCES = ["api.cu", "route.cu", "attn_f32.cu", "attn_tc.cu", "route_static.cu", "balance.cu", "score_tc.cu"]
-HEADERS = ["common.cuh", "route.cuh", "route_dev.cuh", "tc_ptx.cuh", "tmap.cuh"]
+SOURCES = ["api.cu", "route.cu", "attn_f32.cu", "attn_tc.cu", "route_static.cu", "balance.cu", "score_tc.cu",
+           "api_layer.cu", "qk_norm.cu", "dense_f32.cu"]
+HEADERS = ["common.cuh", "route.cuh", "route_dev.cuh", "tc_ptx.cuh", "tmap.cuh", "qk_norm.cuh",
+           "dense.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -10,19 +10,22 @@ using namespace fv;
 
 namespace {
 
-constexpr int kVersion = (1 << 16) | 3;
+constexpr int kVersion = (1 << 16) | 4;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The CUDA error behind the last FVATTN_ERR_CUDA this thread got (fvattn_last_cuda_error).
 thread_local int g_last_cuda_error = 0;
 
-// FVATTN_OK, or FVATTN_ERR_CUDA with the CUDA error recorded for this thread.
-int cuda_status(cudaError_t e) {
+}  // namespace
+
+int fv::cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return FVATTN_OK;
   g_last_cuda_error = (int)e;
   return FVATTN_ERR_CUDA;
 }
+
+namespace {
 
 int validate_shape(const fvattn_shape* s) {
   if (s == nullptr) return FVATTN_ERR_INVALID;

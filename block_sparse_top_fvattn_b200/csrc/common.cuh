@@ -14,6 +14,9 @@ __host__ __device__ __forceinline__ T imin(T a, T b) { return a < b ? a : b; }
 template <typename T>
 __host__ __device__ __forceinline__ T imax(T a, T b) { return a < b ? b : a; }
 
+// FVATTN_OK, or FVATTN_ERR_CUDA with the CUDA error recorded for the calling thread (api.cu).
+int cuda_status(cudaError_t e);
+
 constexpr int kBlock = 64;          // tokens per block (query and key)
 constexpr int kTileRows = 128;      // query rows per attention tile = two query blocks
 

@@ -1,0 +1,516 @@
+// Attention over all keys in fp32 on the CUDA cores, forward and backward, and the two small
+// kernels that the bf16 path shares: the join of split keys and the row sums of out * dout.
+//
+//   s_ij = cap tanh(scale q_i.k_j / cap) - slope |p_i - j|,  P = softmax over the visible j,
+//   out = P V,  lse_i = log sum_j exp(s_ij)
+//   dP = dout V^T,  delta_i = sum_d out_id dout_id,  dX = P (dP - delta) (1 - tanh^2) scale
+//   dQ = dX K,  dK = dX^T Q,  dV = P^T dout
+//
+// A CTA takes 64 rows (forward, dQ) or 64 keys (dK, dV) and walks over the other side in tiles of
+// 64, operands in shared memory as fp32, a 4 x 4 piece of the 64 x 64 scores and a 4 x d/16 piece
+// of each result per thread in registers. Bound by the fp32 pipe and the shared-memory loads that
+// feed it. Every sum has a fixed order.
+#include <cuda_bf16.h>
+
+#include "dense.cuh"
+
+namespace fv {
+
+namespace {
+
+constexpr int kT = 64;            // rows and keys of a tile
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
+
+template <int D>
+struct Tile {
+  static constexpr int kLd = D + 4;        // rows of a tile 16 bytes apart in the banks
+  static constexpr int kFloats = kT * kLd;
+  static constexpr int kLdP = kT + 4;
+  static constexpr int kFloatsP = kT * kLdP;
+};
+
+// Rows row0.. of a key head's (query, head of the group) rows into shared memory; others as zeros.
+template <typename T, int D>
+__device__ __forceinline__ void load_rows(float* dst, const T* base, const fvattn_strides& st, int b, int h0, int G,
+                                          int64_t row0, int64_t nrows) {
+  for (int x = threadIdx.x; x < kT * (D / 4); x += kThreads) {
+    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t rho = row0 + r;
+    if (rho < nrows) v = load4(base + b * st.b + (h0 + rho % G) * st.h + (rho / G) * st.s + c);
+    *reinterpret_cast<float4*>(dst + r * Tile<D>::kLd + c) = v;
+  }
+}
+
+// Keys j0.. below `end` of one key head; others as zeros (whatever they hold). Padding keys too.
+template <typename T, int D>
+__device__ __forceinline__ void load_keys(float* dst, const T* base, const fvattn_strides& st, int b, int h, int j0,
+                                          int end, const int32_t* doc) {
+  for (int x = threadIdx.x; x < kT * (D / 4); x += kThreads) {
+    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int j = j0 + r;
+    if (j < end && (doc == nullptr || doc[j] >= 0)) v = load4(base + b * st.b + h * st.h + (int64_t)j * st.s + c);
+    *reinterpret_cast<float4*>(dst + r * Tile<D>::kLd + c) = v;
+  }
+}
+
+// acc[i][j] = A[ty*4 + i] . B[tx + 16 j] over D.
+template <int D>
+__device__ __forceinline__ void dot_tile(const float* A, const float* B, int ty, int tx, float (&acc)[4][4]) {
+  constexpr int LD = Tile<D>::kLd;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < D; c += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(A + (ty * 4 + i) * LD + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * LD + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
+        acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
+        acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
+        acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+      }
+  }
+}
+
+// acc[i][:] += sum_j W[ty*4 + i][j] X[j][tx*4 + 64 c ..] over the 64 j of a tile.
+template <int D>
+__device__ __forceinline__ void add_product(const float* W, const float* X, int ty, int tx, float (&acc)[4][D / 16]) {
+#pragma unroll 2
+  for (int j = 0; j < kT; j += 4) {
+    float4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty * 4 + i) * Tile<D>::kLdP + j);
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const float4 x = *reinterpret_cast<const float4*>(X + (j + jj) * Tile<D>::kLd + tx * 4 + 64 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float wi = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
+          acc[i][4 * c] = fmaf(wi, x.x, acc[i][4 * c]);
+          acc[i][4 * c + 1] = fmaf(wi, x.y, acc[i][4 * c + 1]);
+          acc[i][4 * c + 2] = fmaf(wi, x.z, acc[i][4 * c + 2]);
+          acc[i][4 * c + 3] = fmaf(wi, x.w, acc[i][4 * c + 3]);
+        }
+      }
+  }
+}
+
+// The capped and biased score of a product x = q.k, and the derivative of the cap.
+__device__ __forceinline__ float score(const DenseArgs& a, const DenseRow& r, float x, int j, float* slope_of_cap) {
+  float s = x * a.scale;
+  *slope_of_cap = 1.f;
+  if (a.cap > 0.f) {
+    const float t = tanhf(s / a.cap);
+    s = a.cap * t;
+    *slope_of_cap = 1.f - t * t;
+  }
+  if (a.mask.slopes != nullptr) s -= r.slope * (float)abs(r.pos - j);
+  return s;
+}
+
+__device__ __forceinline__ float half_warp_max(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// grid: (row tiles * splits, Hkv, B)
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dense_fwd_kernel(const DenseArgs a) {
+  extern __shared__ float sm[];
+  float *sQ = sm, *sK = sQ + Tile<D>::kFloats, *sV = sK + Tile<D>::kFloats, *sP = sV + Tile<D>::kFloats;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int split = blockIdx.x % a.splits, tile = gridDim.x / a.splits - 1 - blockIdx.x / a.splits;
+  const int h = blockIdx.y, b = blockIdx.z, h0 = h * a.G;
+  const int64_t nrows = (int64_t)a.Sq * a.G, row0 = (int64_t)tile * kT;
+  const DenseSeq seq = dense_seq(a, b);
+  const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+  load_rows<T, D>(sQ, static_cast<const T*>(a.q), a.qs, b, h0, a.G, row0, nrows);
+
+  DenseRow row[4];
+  float mx[4], l[4], o[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t rho = row0 + ty * 4 + i;
+    if (rho < nrows)
+      row[i] = dense_row(a, seq, b, h0 + (int)(rho % a.G), (int)(rho / a.G));
+    else
+      row[i] = DenseRow{0, 0, 0, 0.f};
+    mx[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+  }
+  const int64_t last = imin<int64_t>(row0 + kT, nrows) - 1;
+  const int begin = split * a.split_keys;
+  const int end = (int)imin<int64_t>(dense_limit(seq, a.causal, (int)(last / a.G)), (int64_t)begin + a.split_keys);
+  for (int j0 = begin; j0 < end; j0 += kT) {
+    __syncthreads();
+    load_keys<T, D>(sK, static_cast<const T*>(a.k), a.ks, b, h, j0, end, doc_k);
+    load_keys<T, D>(sV, static_cast<const T*>(a.v), a.vs, b, h, j0, end, doc_k);
+    __syncthreads();
+    float s[4][4];
+    dot_tile<D>(sQ, sK, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int j = j0 + tx + 16 * jj;
+        float unused;
+        const bool see = j < row[i].limit && (doc_k == nullptr || doc_k[j] == row[i].doc);
+        s[i][jj] = see ? score(a, row[i], s[i][jj], j, &unused) : -INFINITY;
+        m = fmaxf(m, s[i][jj]);
+      }
+      const float mn = fmaxf(mx[i], half_warp_max(m));
+      const float base = mn == -INFINITY ? 0.f : mn;      // nothing seen so far: weights of 0
+      const float f = expf(mx[i] - base);
+      float add = 0.f;
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const float p = expf(s[i][jj] - base);
+        add += p;
+        sP[(ty * 4 + i) * Tile<D>::kLdP + tx + 16 * jj] = p;
+      }
+      l[i] = l[i] * f + half_warp_sum(add);
+      mx[i] = mn;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
+    }
+    __syncwarp();                // a row's weights are written and read by one half warp
+    add_product<D>(sP, sV, ty, tx, o);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t rho = row0 + ty * 4 + i;
+    if (rho >= nrows) continue;
+    const int hq = h0 + (int)(rho % a.G);
+    const int64_t iq = rho / a.G, flat = ((int64_t)b * a.Hq + hq) * a.Sq + iq;
+    const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+    const float lse = l[i] == 0.f ? -INFINITY : mx[i] + logf(l[i]);
+    if (a.splits > 1) {
+      const int64_t at = (int64_t)split * a.B * a.Hq * a.Sq + flat;
+      float* p = a.part_o + at * D;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) p[tx * 4 + 64 * (c / 4) + c % 4] = o[i][c] * inv;
+      if (tx == 0) a.part_lse[at] = lse;
+    } else {
+      T* p = static_cast<T*>(a.out) + b * a.os.b + hq * a.os.h + iq * a.os.s;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int at = tx * 4 + 64 * (c / 4) + c % 4;
+        const float x = o[i][c] * inv;
+        put(p + at, x);
+        if (a.rest != nullptr) put(static_cast<T*>(a.rest) + (p - static_cast<T*>(a.out)) + at, x - to_f32(p[at]));
+      }
+      if (tx == 0 && a.lse != nullptr) a.lse[flat] = lse;
+    }
+  }
+}
+
+// Joins the splits of a row: weights exp(lse_s - max) in a fixed order. One warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dense_combine_kernel(const DenseArgs a) {
+  const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
+  const int64_t flat = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (flat >= rows) return;
+  float m = -INFINITY;
+  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_lse[s * rows + flat]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+  constexpr int N = D / 32;
+  float acc[N], total = 0.f;
+#pragma unroll
+  for (int c = 0; c < N; ++c) acc[c] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float w = expf(a.part_lse[s * rows + flat] - base);
+    const float* p = a.part_o + (s * rows + flat) * D + lane * N;
+    total += w;
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc[c] = fmaf(w, p[c], acc[c]);
+  }
+  const int64_t iq = flat % a.Sq, bh = flat / a.Sq, b = bh / a.Hq, hq = bh - b * a.Hq;
+  const int64_t at = b * a.os.b + hq * a.os.h + iq * a.os.s + lane * N;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float x = acc[c] * inv;
+    T* p = static_cast<T*>(a.out) + at + c;
+    put(p, x);
+    if (a.rest != nullptr) put(static_cast<T*>(a.rest) + at + c, x - to_f32(*p));
+  }
+  if (lane == 0 && a.lse != nullptr) a.lse[flat] = total == 0.f ? -INFINITY : m + logf(total);
+}
+
+// delta = sum_d (out + rest) dout, one warp per row. Padding queries get 0, whatever they hold.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dense_delta_kernel(const DenseArgs a) {
+  const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
+  const int64_t flat = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (flat >= rows) return;
+  const int64_t iq = flat % a.Sq, bh = flat / a.Sq, b = bh / a.Hq, hq = bh - b * a.Hq;
+  constexpr int N = D / 32;
+  const int64_t at = b * a.os.b + hq * a.os.h + iq * a.os.s + lane * N;
+  const T* o = static_cast<const T*>(a.out) + at;
+  const T* r = a.rest != nullptr ? static_cast<const T*>(a.rest) + at : nullptr;
+  const T* g = static_cast<const T*>(a.dout) + b * a.dos.b + hq * a.dos.h + iq * a.dos.s + lane * N;
+  float acc = 0.f;
+#pragma unroll
+  for (int c = 0; c < N; ++c) acc = fmaf(to_f32(o[c]) + (r != nullptr ? to_f32(r[c]) : 0.f), to_f32(g[c]), acc);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
+  const bool pad = a.mask.doc_q != nullptr && a.mask.doc_q[b * a.Sq + iq] < 0;
+  if (lane == 0) a.delta[flat] = pad ? 0.f : acc;
+}
+
+// Probability and score gradient of one pair: p = exp(s - lse), ds = p (dp - delta) cap' scale.
+__device__ __forceinline__ void pair_grads(const DenseArgs& a, const DenseRow& r, float lse, float delta, float x,
+                                           float dp, int j, const int32_t* doc_k, float* p, float* ds) {
+  *p = 0.f;
+  *ds = 0.f;
+  if (j < r.limit && (doc_k == nullptr || doc_k[j] == r.doc)) {
+    float dcap;
+    const float s = score(a, r, x, j, &dcap);
+    *p = expf(s - lse);
+    *ds = *p * (dp - delta) * dcap * a.scale;
+  }
+}
+
+// grid: (row tiles, Hkv, B)
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dense_dq_kernel(const DenseArgs a) {
+  extern __shared__ float sm[];
+  float *sQ = sm, *sG = sQ + Tile<D>::kFloats, *sK = sG + Tile<D>::kFloats, *sV = sK + Tile<D>::kFloats,
+        *sP = sV + Tile<D>::kFloats;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int tile = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z, h0 = h * a.G;
+  const int64_t nrows = (int64_t)a.Sq * a.G, row0 = (int64_t)tile * kT;
+  const DenseSeq seq = dense_seq(a, b);
+  const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+  load_rows<T, D>(sQ, static_cast<const T*>(a.q), a.qs, b, h0, a.G, row0, nrows);
+  load_rows<T, D>(sG, static_cast<const T*>(a.dout), a.dos, b, h0, a.G, row0, nrows);
+  DenseRow row[4];
+  float lse[4], delta[4], dq[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t rho = row0 + ty * 4 + i;
+    row[i] = DenseRow{0, 0, 0, 0.f};
+    lse[i] = delta[i] = 0.f;
+    if (rho < nrows) {
+      const int hq = h0 + (int)(rho % a.G);
+      const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + rho / a.G;
+      row[i] = dense_row(a, seq, b, hq, (int)(rho / a.G));
+      lse[i] = a.lse[flat];
+      delta[i] = a.delta[flat];
+    }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) dq[i][c] = 0.f;
+  }
+  const int64_t last = imin<int64_t>(row0 + kT, nrows) - 1;
+  const int end = dense_limit(seq, a.causal, (int)(last / a.G));
+  for (int j0 = 0; j0 < end; j0 += kT) {
+    __syncthreads();
+    load_keys<T, D>(sK, static_cast<const T*>(a.k), a.ks, b, h, j0, end, doc_k);
+    load_keys<T, D>(sV, static_cast<const T*>(a.v), a.vs, b, h, j0, end, doc_k);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    dot_tile<D>(sQ, sK, ty, tx, s);
+    dot_tile<D>(sG, sV, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        float p, ds;
+        pair_grads(a, row[i], lse[i], delta[i], s[i][jj], dp[i][jj], j0 + tx + 16 * jj, doc_k, &p, &ds);
+        sP[(ty * 4 + i) * Tile<D>::kLdP + tx + 16 * jj] = ds;
+      }
+    __syncwarp();
+    add_product<D>(sP, sK, ty, tx, dq);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t rho = row0 + ty * 4 + i;
+    if (rho >= nrows) continue;
+    T* p = static_cast<T*>(a.dq) + b * a.dqs.b + (h0 + rho % a.G) * a.dqs.h + (rho / a.G) * a.dqs.s;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) put(p + tx * 4 + 64 * (c / 4) + c % 4, dq[i][c]);
+  }
+}
+
+// grid: (key tiles, Hkv, B)
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dense_dkv_kernel(const DenseArgs a) {
+  extern __shared__ float sm[];
+  float *sK = sm, *sV = sK + Tile<D>::kFloats, *sQ = sV + Tile<D>::kFloats, *sG = sQ + Tile<D>::kFloats,
+        *sP = sG + Tile<D>::kFloats, *sS = sP + Tile<D>::kFloatsP;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int j0 = blockIdx.x * kT, h = blockIdx.y, b = blockIdx.z, h0 = h * a.G;
+  const int64_t nrows = (int64_t)a.Sq * a.G;
+  const DenseSeq seq = dense_seq(a, b);
+  const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+  load_keys<T, D>(sK, static_cast<const T*>(a.k), a.ks, b, h, j0, seq.kv, doc_k);
+  load_keys<T, D>(sV, static_cast<const T*>(a.v), a.vs, b, h, j0, seq.kv, doc_k);
+  float dk[4][D / 16], dv[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
+  for (int64_t row0 = 0; row0 < nrows; row0 += kT) {
+    const int64_t last = imin<int64_t>(row0 + kT, nrows) - 1;
+    if (dense_limit(seq, a.causal, (int)(last / a.G)) <= j0) continue;    // the same for the whole CTA
+    __syncthreads();
+    load_rows<T, D>(sQ, static_cast<const T*>(a.q), a.qs, b, h0, a.G, row0, nrows);
+    load_rows<T, D>(sG, static_cast<const T*>(a.dout), a.dos, b, h0, a.G, row0, nrows);
+    __syncthreads();
+    // scores as [key][row]: this thread's four keys, four rows
+    float s[4][4], dp[4][4];
+    dot_tile<D>(sK, sQ, ty, tx, s);
+    dot_tile<D>(sV, sG, ty, tx, dp);
+#pragma unroll
+    for (int rr = 0; rr < 4; ++rr) {
+      const int64_t rho = row0 + tx + 16 * rr;
+      DenseRow row{0, 0, 0, 0.f};
+      float lse = 0.f, delta = 0.f;
+      if (rho < nrows) {
+        const int hq = h0 + (int)(rho % a.G);
+        const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + rho / a.G;
+        row = dense_row(a, seq, b, hq, (int)(rho / a.G));
+        lse = a.lse[flat];
+        delta = a.delta[flat];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float p, ds;
+        pair_grads(a, row, lse, delta, s[i][rr], dp[i][rr], j0 + ty * 4 + i, doc_k, &p, &ds);
+        sP[(ty * 4 + i) * Tile<D>::kLdP + tx + 16 * rr] = p;
+        sS[(ty * 4 + i) * Tile<D>::kLdP + tx + 16 * rr] = ds;
+      }
+    }
+    // a padding query may hold anything: its row must not reach the products below
+    if (a.mask.doc_q != nullptr) {
+      __syncthreads();
+      for (int r = threadIdx.x; r < kT; r += kThreads) {
+        const int64_t rho = row0 + r;
+        if (rho < nrows && a.mask.doc_q[(int64_t)b * a.Sq + rho / a.G] < 0)
+          for (int c = 0; c < D; ++c) sQ[r * Tile<D>::kLd + c] = sG[r * Tile<D>::kLd + c] = 0.f;
+      }
+      __syncthreads();
+    } else {
+      __syncwarp();
+    }
+    add_product<D>(sP, sG, ty, tx, dv);
+    add_product<D>(sS, sQ, ty, tx, dk);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = j0 + ty * 4 + i;
+    if (j >= a.Sk) continue;
+    T* pk = static_cast<T*>(a.dk) + b * a.dks.b + h * a.dks.h + (int64_t)j * a.dks.s;
+    T* pv = static_cast<T*>(a.dv) + b * a.dvs.b + h * a.dvs.h + (int64_t)j * a.dvs.s;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      put(pk + tx * 4 + 64 * (c / 4) + c % 4, dk[i][c]);
+      put(pv + tx * 4 + 64 * (c / 4) + c % 4, dv[i][c]);
+    }
+  }
+}
+
+template <typename K>
+cudaError_t run(K kernel, dim3 grid, size_t smem, const DenseArgs& a, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+unsigned row_tiles(const DenseArgs& a) { return (unsigned)(((int64_t)a.Sq * a.G + kT - 1) / kT); }
+
+template <typename T, int D>
+cudaError_t fwd_d(const DenseArgs& a, cudaStream_t st) {
+  const size_t smem = (3 * Tile<D>::kFloats + Tile<D>::kFloatsP) * sizeof(float);
+  return run(dense_fwd_kernel<T, D>, dim3(row_tiles(a) * a.splits, a.Hkv, a.B), smem, a, st);
+}
+
+template <typename T, int D>
+cudaError_t bwd_d(const DenseArgs& a, cudaStream_t st) {
+  const size_t smem = (4 * Tile<D>::kFloats + 2 * Tile<D>::kFloatsP) * sizeof(float);
+  const cudaError_t e = run(dense_dq_kernel<T, D>, dim3(row_tiles(a), a.Hkv, a.B), smem, a, st);
+  if (e != cudaSuccess) return e;
+  return run(dense_dkv_kernel<T, D>, dim3((unsigned)((a.Sk + kT - 1) / kT), a.Hkv, a.B), smem, a, st);
+}
+
+unsigned warp_rows(const DenseArgs& a) {
+  return (unsigned)(((int64_t)a.B * a.Hq * a.Sq + kThreads / 32 - 1) / (kThreads / 32));
+}
+
+}  // namespace
+
+cudaError_t launch_dense_f32(const DenseArgs& a, cudaStream_t st) {
+  return a.d == 128 ? fwd_d<float, 128>(a, st) : fwd_d<float, 64>(a, st);
+}
+cudaError_t launch_dense_f32_bwd(const DenseArgs& a, cudaStream_t st) {
+  return a.d == 128 ? bwd_d<float, 128>(a, st) : bwd_d<float, 64>(a, st);
+}
+cudaError_t launch_dense_simple_bf16(const DenseArgs& a, cudaStream_t st) {
+  return a.d == 128 ? fwd_d<__nv_bfloat16, 128>(a, st) : fwd_d<__nv_bfloat16, 64>(a, st);
+}
+cudaError_t launch_dense_simple_bf16_bwd(const DenseArgs& a, cudaStream_t st) {
+  return a.d == 128 ? bwd_d<__nv_bfloat16, 128>(a, st) : bwd_d<__nv_bfloat16, 64>(a, st);
+}
+
+cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st) {
+  if (dtype == FVATTN_F32) {
+    if (a.d == 128) dense_combine_kernel<float, 128><<<warp_rows(a), kThreads, 0, st>>>(a);
+    else dense_combine_kernel<float, 64><<<warp_rows(a), kThreads, 0, st>>>(a);
+  } else {
+    if (a.d == 128) dense_combine_kernel<__nv_bfloat16, 128><<<warp_rows(a), kThreads, 0, st>>>(a);
+    else dense_combine_kernel<__nv_bfloat16, 64><<<warp_rows(a), kThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dense_delta(const DenseArgs& a, int dtype, cudaStream_t st) {
+  if (dtype == FVATTN_F32) {
+    if (a.d == 128) dense_delta_kernel<float, 128><<<warp_rows(a), kThreads, 0, st>>>(a);
+    else dense_delta_kernel<float, 64><<<warp_rows(a), kThreads, 0, st>>>(a);
+  } else {
+    if (a.d == 128) dense_delta_kernel<__nv_bfloat16, 128><<<warp_rows(a), kThreads, 0, st>>>(a);
+    else dense_delta_kernel<__nv_bfloat16, 64><<<warp_rows(a), kThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fv

@@ -357,6 +357,135 @@ int fvattn_route_static_scratch(const void* Q, const void* K, const fvattn_shape
                                 const fvattn_route_cfg* cfg, const fvattn_csr* out,
                                 fvattn_stream_t stream);
 
+/*
+ * ------------------------------------------------------------------------------------------
+ * Around the layer: the operators that prepare its queries and keys and that attend to all
+ * keys, each with its gradients. The pages leave them to the host model. Their tensors may be
+ * strided: the last dimension is contiguous, and the strides of the others, in elements, are
+ * multiples of 16 bytes and positive (the stride of a dimension of size 1 is not read). Bases
+ * are 16-byte aligned. Outputs must not overlap inputs or one another.
+ * `status` (device int32[4], or NULL: not reported) is not cleared by these calls: the caller
+ * zeroes it once, the first error found on the device is kept (status[0] the fvattn_status,
+ * status[1] a detail), and the rows concerned are written as NaN.
+ */
+typedef struct { int64_t b, h, s; } fvattn_strides;   /* of batch, head and token, in elements */
+
+/*
+ * Per-head RMS norm and position rotation of queries and keys.
+ *  B, S, Hq, Hk, d   tokens and heads; d 64 or 128. Hq and Hk need not be equal.
+ *  dtype             of q, k and their outputs and gradients (fvattn_dtype).
+ *  weight_dtype      of the norm weights.
+ *  rot               leading elements of a head that are rotated: 0, or a multiple of 16 up to d.
+ *  interleaved       1: the pairs turned together are elements (2i, 2i+1); 0: (i, i + rot/2).
+ *  eps               added to the mean square, finite and >= 0.
+ *  table_rows        rows of the cosine and sine tables.
+ *  q, k              strides of the projections (and, in the gradients' call, qo and ko are those
+ *  qo, ko            of the output gradients, dq and dk those of the gradients of q and k).
+ */
+typedef struct {
+  int64_t B, S, Hq, Hk, d;
+  int32_t dtype, weight_dtype, rot, interleaved;
+  float eps;
+  int64_t table_rows;
+  fvattn_strides q, k, qo, ko, dq, dk;
+} fvattn_qk_shape;
+
+/*
+ * fvattn_qk_norm_rope -- for every head row x of q and k, with r = 1/sqrt(mean(x^2) + eps):
+ *   y = R(position) (x * r * w),
+ * R turning each pair (a, b) of the first rot elements into (a cos - b sin, a sin + b cos).
+ * q: [B, S, Hq, d], k: [B, S, Hk, d] in any strides (slices of one projection's output are fine);
+ * qo: [B, Hq, S, d], ko: [B, Hk, S, d] in any strides: dense for fvattn_route and
+ * fvattn_sparse_attn, or a place in a longer cache. wq, wk: device [d] or NULL (ones).
+ * cos, sin: device float [table_rows, rot/2] (NULL when rot is 0). positions: device int32
+ * [B, S], the table row of each token, or NULL (token s uses row s; table_rows >= S then).
+ * A position outside the tables makes its rows NaN (detail 201, FVATTN_ERR_INVALID). The
+ * arithmetic is fp32, rounded once at the end.
+ *
+ * fvattn_qk_norm_rope_bwd -- with g = R^T dy: dx = r (g w) - x r^3 mean(g w x), and
+ * dw = sum over all rows of g r x. gq, gk: gradients of qo and ko; dq, dk: as q and k. dwq, dwk:
+ * device float [d] or NULL; summed in a fixed order, so equal calls give equal bits.
+ * workspace: 16-byte aligned, fvattn_qk_norm_rope_workspace_bytes(shape) bytes (0 on invalid
+ * arguments; host only).
+ */
+int fvattn_qk_norm_rope(const void* q, const void* k, const fvattn_qk_shape* shape, const void* wq,
+                        const void* wk, const float* cos, const float* sin, const int32_t* positions,
+                        void* qo, void* ko, int32_t* status, fvattn_stream_t stream);
+size_t fvattn_qk_norm_rope_workspace_bytes(const fvattn_qk_shape* shape);
+int fvattn_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, const void* k,
+                            const fvattn_qk_shape* shape, const void* wq, const void* wk,
+                            const float* cos, const float* sin, const int32_t* positions, void* dq,
+                            void* dk, float* dwq, float* dwk, void* workspace,
+                            size_t workspace_bytes, int32_t* status, fvattn_stream_t stream);
+
+/*
+ * Attention over all keys.
+ *  B, Hq, Hkv, Sq, Sk, d  Hq a multiple of Hkv, at most 128 times it (query head h reads key head
+ *                    h / (Hq / Hkv)); Sq and Sk independent, >= 1; d 64 or 128.
+ *  dtype             fvattn_dtype. scale: <= 0 means 1/sqrt(d).
+ *  softcap           0, or c > 0: scores become c tanh(score / c).
+ *  causal            1: key j is visible to the query at position p when j <= p, or when
+ *                    j < prefix_len of its sequence.
+ *  q, k, v, o        strides of q, k, v and out (rest has out's); dout, dq, dk, dv: the gradients'.
+ */
+typedef struct {
+  int64_t B, Hq, Hkv, Sq, Sk, d;
+  int32_t dtype;
+  float scale;
+  float softcap;
+  int32_t causal;
+  fvattn_strides q, k, v, o, dout, dq, dk, dv;
+} fvattn_dense_shape;
+
+/*
+ * What biases and masks the scores; every pointer is a device array or NULL.
+ *  slopes      float [Hq]: the score of (query position p, key j) falls by slope * |p - j| (after
+ *              the cap).
+ *  q_start     int32 [B]: position of a sequence's first query; NULL: Sk - Sq.
+ *  kv_len      int32 [B]: keys from kv_len on do not exist (their K and V are never used, whatever
+ *              they hold); values outside [0, Sk] are clamped. NULL: Sk.
+ *  prefix_len  int32 [B]: with causal, keys below it are visible to every query.
+ *  doc_q, doc_k int32 [B, Sq] and [B, Sk], both or neither: a query sees only keys of an equal
+ *              document number; a negative number is padding, sees nothing and is seen by nothing
+ *              (padding queries, keys and output gradients may hold anything).
+ */
+typedef struct {
+  const float* slopes;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* prefix_len;
+  const int32_t* doc_q;
+  const int32_t* doc_k;
+} fvattn_dense_mask;
+
+/*
+ * fvattn_dense_attn -- out[i] = sum_j softmax_j(s_ij) V[j] over the keys visible to query i, with
+ *   s_ij = cap(Q[i].K[j] * scale) - slope |p_i - j|.
+ * A row that sees no key is written as zeros, with lse = -inf. lse: float [B, Hq, Sq] (dense), the
+ * natural-log normaliser of each row, or NULL. rest: NULL, or a bf16 tensor like out (bf16 only)
+ * that receives what out's rounding left over: out + rest is the result to 16 bits, which the
+ * gradients of short or sharply peaked rows need. Few queries over many keys (single tokens over
+ * a cache) are split over the keys and joined. mask: NULL for none. workspace: 256-byte aligned,
+ * fvattn_dense_attn_workspace_bytes(shape, mask) bytes (may be 0; (size_t)-1 on invalid
+ * arguments; host only).
+ *
+ * fvattn_dense_attn_bwd -- gradients of out with respect to q, k and v for the output gradient
+ * dout, from the forward call's out, rest (or NULL) and lse (required). Shared key heads receive the sum
+ * over their query heads. Sums are made in fp32 in a fixed order: equal calls give equal bits.
+ * workspace as above, fvattn_dense_attn_bwd_workspace_bytes(shape, mask) bytes.
+ */
+size_t fvattn_dense_attn_workspace_bytes(const fvattn_dense_shape* shape, const fvattn_dense_mask* mask);
+int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_dense_shape* shape,
+                      const fvattn_dense_mask* mask, void* out, void* rest, float* lse,
+                      void* workspace, size_t workspace_bytes, int32_t* status,
+                      fvattn_stream_t stream);
+size_t fvattn_dense_attn_bwd_workspace_bytes(const fvattn_dense_shape* shape, const fvattn_dense_mask* mask);
+int fvattn_dense_attn_bwd(const void* dout, const void* q, const void* k, const void* v,
+                          const void* out, const void* rest, const float* lse,
+                          const fvattn_dense_shape* shape, const fvattn_dense_mask* mask, void* dq,
+                          void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                          int32_t* status, fvattn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
