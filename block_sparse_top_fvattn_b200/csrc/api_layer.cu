@@ -139,10 +139,13 @@ size_t take(size_t& off, size_t bytes) {
 }
 
 struct DenseWs {
-  size_t part_o, part_lse, delta, total;
+  size_t part_o, part_lse, delta, docs_q, docs_k, total;
 };
 
-DenseWs fwd_ws(const DenseArgs& a) {
+bool uses_tc(const DenseArgs&, int dtype) { return dtype == FVATTN_BF16; }
+size_t doc_bytes(int64_t B, int64_t S) { return (size_t)(B * ((S + kBlock - 1) / kBlock)) * sizeof(int2); }
+
+DenseWs fwd_ws(const DenseArgs& a, int dtype) {
   DenseWs w{};
   size_t off = 0;
   const size_t rows = (size_t)a.B * a.Hq * a.Sq;
@@ -150,6 +153,7 @@ DenseWs fwd_ws(const DenseArgs& a) {
     w.part_o = take(off, rows * a.splits * a.d * sizeof(float));
     w.part_lse = take(off, rows * a.splits * sizeof(float));
   }
+  if (uses_tc(a, dtype) && a.mask.doc_k != nullptr) w.docs_k = take(off, doc_bytes(a.B, a.Sk));
   w.total = off;
   return w;
 }
@@ -164,14 +168,13 @@ DenseWs bwd_ws(const DenseArgs& a) {
 
 DenseArgs fwd_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
   DenseArgs a = dense_args(s, m);
-  plan_splits(a, imax(1, 64 / a.G));
+  plan_splits(a, s->dtype == FVATTN_F32 ? imax(1, 64 / a.G) : kTileRows / a.G);
   return a;
 }
 
 }  // namespace
 
 namespace fv {
-cudaError_t launch_dense_simple_bf16(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_simple_bf16_bwd(const DenseArgs& a, cudaStream_t st);
 }  // namespace fv
 
@@ -242,7 +245,7 @@ int fvattn_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, const
 
 size_t fvattn_dense_attn_workspace_bytes(const fvattn_dense_shape* shape, const fvattn_dense_mask* mask) {
   if (validate_dense(shape, mask, false) != FVATTN_OK) return (size_t)-1;
-  return fwd_ws(fwd_args(shape, mask)).total;
+  return fwd_ws(fwd_args(shape, mask), shape->dtype).total;
 }
 
 int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_dense_shape* shape,
@@ -256,7 +259,7 @@ int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_
   if (!aligned(lse, 4) || !aligned(status, 4)) return FVATTN_ERR_INVALID;
   if (rest != nullptr && shape->dtype != FVATTN_BF16) return FVATTN_ERR_INVALID;
   DenseArgs a = fwd_args(shape, mask);
-  const DenseWs w = fwd_ws(a);
+  const DenseWs w = fwd_ws(a, shape->dtype);
   if (w.total > 0 && (workspace == nullptr || !aligned(workspace, 256))) return FVATTN_ERR_INVALID;
   if (workspace_bytes < w.total) return FVATTN_ERR_CAPACITY;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -272,7 +275,12 @@ int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_
     a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = shape->dtype == FVATTN_F32 ? launch_dense_f32(a, s) : launch_dense_simple_bf16(a, s);
+  cudaError_t e = cudaSuccess;
+  if (uses_tc(a, shape->dtype) && a.mask.doc_k != nullptr) {
+    a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
+    e = launch_dense_docs(a, false, s);
+  }
+  if (e == cudaSuccess) e = uses_tc(a, shape->dtype) ? launch_dense_tc(a, s) : launch_dense_f32(a, s);
   if (e == cudaSuccess && a.splits > 1) e = launch_dense_combine(a, shape->dtype, s);
   return cuda_status(e);
 }

@@ -29,7 +29,7 @@ struct DenseArgs {
   int splits, split_keys;         // forward: the keys in `splits` ranges of split_keys (a multiple of 64)
   float *part_o, *part_lse;       // splits > 1: [splits][B][Hq][Sq][d] and [splits][B][Hq][Sq]
   float* delta;                   // backward: [B][Hq][Sq], sum_d out * dout
-  uint32_t* need;                 // documents: see need_words()
+  int2 *doc_blocks_q, *doc_blocks_k;   // documents of the 64-token blocks (dense_doc_kernel)
   int32_t* status;
 };
 
@@ -77,6 +77,8 @@ __device__ __forceinline__ DenseRow dense_row(const DenseArgs& a, const DenseSeq
 }
 
 // Launchers. Each returns the launch's error.
+cudaError_t launch_dense_docs(const DenseArgs& a, bool queries, cudaStream_t st);
+cudaError_t launch_dense_tc(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_f32(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_dense_delta(const DenseArgs& a, int dtype, cudaStream_t st);

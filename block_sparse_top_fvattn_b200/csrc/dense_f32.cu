@@ -296,6 +296,33 @@ __global__ void __launch_bounds__(kThreads) dense_delta_kernel(const DenseArgs a
   if (lane == 0) a.delta[flat] = pad ? 0.f : acc;
 }
 
+// The documents of each 64-token block of doc [B][S], one warp per block: see doc_low().
+__global__ void __launch_bounds__(kThreads) dense_doc_kernel(const int32_t* doc, int2* blocks, int B, int S) {
+  const int nb = (S + kBlock - 1) / kBlock, lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (w >= (int64_t)B * nb) return;
+  const int64_t b = w / nb, j = w - b * nb;
+  int lo = 0x7fffffff, hi = -1;
+  bool pad = false;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t t = j * kBlock + u * 32 + lane;
+    if (t < S) {
+      const int v = doc[b * S + t];
+      if (v < 0) {
+        pad = true;
+      } else {
+        lo = min(lo, v);
+        hi = max(hi, v);
+      }
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  pad = __any_sync(0xffffffffu, pad);
+  if (lane == 0) blocks[w] = make_int2(pad ? (int)((uint32_t)lo | 0x80000000u) : lo, hi);
+}
+
 // Probability and score gradient of one pair: p = exp(s - lse), ds = p (dp - delta) cap' scale.
 __device__ __forceinline__ void pair_grads(const DenseArgs& a, const DenseRow& r, float lse, float delta, float x,
                                            float dp, int j, const int32_t* doc_k, float* p, float* ds) {
@@ -489,6 +516,14 @@ cudaError_t launch_dense_simple_bf16(const DenseArgs& a, cudaStream_t st) {
 }
 cudaError_t launch_dense_simple_bf16_bwd(const DenseArgs& a, cudaStream_t st) {
   return a.d == 128 ? bwd_d<__nv_bfloat16, 128>(a, st) : bwd_d<__nv_bfloat16, 64>(a, st);
+}
+
+cudaError_t launch_dense_docs(const DenseArgs& a, bool queries, cudaStream_t st) {
+  const int S = queries ? a.Sq : a.Sk;
+  const int64_t warps = (int64_t)a.B * ((S + kBlock - 1) / kBlock);
+  dense_doc_kernel<<<(unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(
+      queries ? a.mask.doc_q : a.mask.doc_k, queries ? a.doc_blocks_q : a.doc_blocks_k, a.B, S);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st) {

@@ -1,0 +1,439 @@
+// Attention over all keys on the B200 tensor cores (tcgen05, TMEM, TMA): bf16 inputs, fp32 scores,
+// softmax statistics and sums.
+//
+//   s_ij = cap tanh(scale q_i.k_j / cap) - slope |p_i - j|, out_i = sum_j softmax_j(s_ij) v_j
+//
+// One CTA takes 128 rows of one key head (row i * G + g: query i of the group's head g, so that shared
+// keys are read once) and one range of its keys, in blocks of 64 keys; for each block j
+//   S = Q K_j^T          tcgen05.mma M=128 N=64 K=d, fp32 in TMEM, two buffers
+//   P = exp2(s - m)      one thread per row: cap, bias and mask of its row, running maximum m that is
+//                        raised (with a rescale of O in TMEM) only when it grows by more than 2^8,
+//                        P as bf16 over its S buffer
+//   O += P V_j           tcgen05.mma M=128 N=d K=64, P read from TMEM
+// Two CTAs share an SM, so one's softmax runs beside the other's products. Blocks that no row of the
+// tile can see (behind the limit of its last query, or of other documents) are not visited.
+// A few queries over many keys leave most rows empty: the warps of empty rows skip the softmax, the
+// keys are split over CTAs, and the partial results are joined by a second kernel.
+//
+// Rounding P to bf16 is what the second product's operands need; the row sums are of the unrounded P.
+//
+// Every wait is bounded; one that runs out stops every role without leaving a copy or product in
+// flight, is reported in the status word, and makes the tile's rows NaN.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "dense.cuh"
+#include "dense_tc.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.cuh"
+
+namespace fv {
+
+namespace {
+
+constexpr int NS = 2;          // stages of K and of V; the stage of a step is also its S / P buffer
+constexpr int kWarps = 7;      // K loader, MMA, four softmax warps, V loader
+constexpr float kRescaleLog2 = 8.0f;
+
+template <int D>
+struct FwdLayout {
+  static constexpr int kQChunk = kTileRows * 128;     // [128 rows x 64 dims] bf16
+  static constexpr int kQBytes = (D / 64) * kQChunk;
+  static constexpr int kKVChunk = kBlock * 128;       // [64 keys x 64 dims] bf16
+  static constexpr int kKBytes = (D / 64) * kKVChunk;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kQBytes;
+  static constexpr int kOffV = kOffK + NS * kKBytes;
+  static constexpr int kOffBar = kOffV + NS * kKBytes;
+  static constexpr int kBytes = kOffBar + 256;
+  static constexpr uint32_t kTmemCols = 256;          // S / P buffers at 0 and 64, O at 128
+  static constexpr uint32_t kColO = 128;
+};
+
+struct FwdBars {
+  uint64_t q_full;
+  uint64_t k_full[NS];
+  uint64_t s_full[2];     // S of a step done: the softmax may read it, its K stage may be refilled
+  uint64_t p_full[2];     // P written by the four softmax warps and V landed (the V loader's arrival)
+  uint64_t pv_done[2];    // P V done: O is stable, the V stage may be refilled
+  uint64_t drain;         // every product of the CTA is done
+  int p_arrived[4];       // per softmax warp: the last step whose P it published
+  int v_armed;            // the last step whose V copy was issued
+  int doc_lo, doc_hi;     // documents of the tile's rows
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    dense_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const DenseArgs a, const int qpt) {
+  using L = FwdLayout<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  FwdBars* bars = reinterpret_cast<FwdBars*>(smem + L::kOffBar);
+  unsigned char* sQ = smem + L::kOffQ;
+  unsigned char* sK = smem + L::kOffK;
+  unsigned char* sV = smem + L::kOffV;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &bars->abort;
+
+  const int split = blockIdx.x % a.splits;
+  const int t = gridDim.x / a.splits - 1 - blockIdx.x / a.splits;     // the longest tiles first under an order
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int i0 = t * qpt, i1 = min(i0 + qpt, a.Sq);                   // this tile's queries
+  const DenseSeq seq = dense_seq(a, b);
+  const int key0 = split * a.split_keys;
+  const int key1 = (int)imin<int64_t>(dense_limit(seq, a.causal, i1 - 1), (int64_t)key0 + a.split_keys);
+
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->q_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&bars->k_full[s], 1);
+      tc::mbar_init(&bars->s_full[s], 1);
+      tc::mbar_init(&bars->p_full[s], 5);
+      tc::mbar_init(&bars->pv_done[s], 1);
+    }
+    tc::mbar_init(&bars->drain, 1);
+    for (int w = 0; w < 4; ++w) bars->p_arrived[w] = -1;
+    bars->v_armed = -1;
+    bars->abort = 0;
+    bars->doc_lo = 0x7fffffff;
+    bars->doc_hi = -1;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&bars->tmem_base, L::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::prefetch_tmap(&tmQ);
+    tc::prefetch_tmap(&tmK);
+    tc::prefetch_tmap(&tmV);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (a.mask.doc_q != nullptr) {
+    for (int i = i0 + threadIdx.x; i < i1; i += kWarps * 32) {
+      const int doc = a.mask.doc_q[(int64_t)b * a.Sq + i];
+      if (doc >= 0) {
+        atomicMin(&bars->doc_lo, doc);
+        atomicMax(&bars->doc_hi, doc);
+      }
+    }
+    __syncthreads();
+  }
+  const uint32_t tbase = bars->tmem_base;
+  BlockWalk walk(a, b, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ Q and K loader
+    int k_par[NS] = {-1, -1};
+    bool q_armed = false;
+    uint32_t g = 0;
+    for (int j; (j = walk.next(lane)) >= 0; ++g) {
+      int ok = 1;
+      if (lane == 0) {
+        if (g == 0) {
+          tc::mbar_expect_tx(&bars->q_full, (uint32_t)(qpt * a.G) * 128 * (D / 64));
+          q_armed = true;
+          for (int c = 0; c < D / 64; ++c)
+            tc::tma_load_5d(sQ + c * L::kQChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
+        }
+        const int st = g % NS;
+        if (!tc::mbar_wait(&bars->s_full[st], ((g / NS) & 1) ^ 1, abort, kWaitLimit)) {
+          fail(&bars->abort, 3);
+          ok = 0;
+        } else {
+          tc::mbar_expect_tx(&bars->k_full[st], L::kKBytes);
+          k_par[st] = (g / NS) & 1;
+          for (int c = 0; c < D / 64; ++c)
+            tc::tma_load_4d(sK + st * L::kKBytes + c * L::kKVChunk, &tmK, &bars->k_full[st], c * 64, j * kBlock, h, b);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    }
+    // no copy may still be writing shared memory when the CTA leaves
+    if (lane == 0) {
+      if (q_armed) tc::mbar_wait_drain(&bars->q_full, 0, kWaitLimit);
+      for (int st = 0; st < NS; ++st)
+        if (k_par[st] >= 0) tc::mbar_wait_drain(&bars->k_full[st], (uint32_t)k_par[st], kWaitLimit);
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------------------------ V loader
+    uint32_t g = 0;
+    for (int j; (j = walk.next(lane)) >= 0; ++g) {
+      const int st = g % NS;
+      if (!warp_wait(&bars->pv_done[st], ((g / NS) & 1) ^ 1, abort)) {
+        fail(&bars->abort, 16);
+        break;
+      }
+      unsigned char* dst = sV + st * L::kKBytes;
+      if (dirty_block(a, seq, b, j)) {
+        // keys that do not exist: zeros, whatever their memory holds (0 * NaN would reach O)
+        copy_keys<D>(dst, static_cast<const __nv_bfloat16*>(a.v) + b * a.vs.b + h * a.vs.h, a.vs.s, j * kBlock, kBlock,
+                     seq.kv, a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr, lane, 32);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&bars->p_full[st]);
+          *reinterpret_cast<volatile int*>(&bars->v_armed) = (int)g;
+        }
+      } else if (lane == 0) {
+        tc::mbar_expect_tx(&bars->p_full[st], L::kKBytes);
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_4d(dst + c * L::kKVChunk, &tmV, &bars->p_full[st], c * 64, j * kBlock, h, b);
+        *reinterpret_cast<volatile int*>(&bars->v_armed) = (int)g;
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    // Order: S_0, [S_1, PV_0], [S_2, PV_1], ..., PV_last. Products of one thread run in issue order,
+    // so S_{g+2} (the buffer of S_g and P_g) always follows PV_g.
+    const uint32_t n = (uint32_t)walk.count(lane);
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idS = tc::idesc_bf16_f32(kTileRows, kBlock, 0, 0);
+      constexpr uint32_t idO = tc::idesc_bf16_f32(kTileRows, D, 0, 1);
+      const uint32_t qaddr = tc::smem_u32(sQ), kaddr0 = tc::smem_u32(sK), vaddr0 = tc::smem_u32(sV);
+      auto pv = [&](uint32_t g) -> bool {
+        const int pb = g & 1;
+        if (!tc::mbar_wait(&bars->p_full[pb], (g >> 1) & 1, abort, kWaitLimit)) return false;
+        tc::fence_after_sync();
+        const uint32_t vaddr = vaddr0 + pb * L::kKBytes;
+#pragma unroll
+        for (int kk = 0; kk < kBlock / 16; ++kk) {
+          const uint64_t bd = tc::smem_desc_sw128(vaddr + kk * 16 * 128, L::kKVChunk, 1024);
+          tc::mma_f16_tmem_a(tbase + L::kColO, tbase + pb * kBlock + kk * 8, bd, idO, (g == 0 && kk == 0) ? 0u : 1u);
+        }
+        tc::mma_commit(&bars->pv_done[pb]);
+        return true;
+      };
+      if (!tc::mbar_wait(&bars->q_full, 0, abort, kWaitLimit)) {
+        fail(&bars->abort, 5);
+      } else {
+        uint32_t g = 0;
+        for (; g < n; ++g) {
+          const int st = g % NS;
+          if (!tc::mbar_wait(&bars->k_full[st], (g / NS) & 1, abort, kWaitLimit)) {
+            fail(&bars->abort, 6);
+            break;
+          }
+          tc::fence_after_sync();
+          const uint32_t kaddr = kaddr0 + st * L::kKBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int c = kk >> 2, off = (kk & 3) * 32;
+            const uint64_t ad = tc::smem_desc_sw128(qaddr + c * L::kQChunk + off, 16, 1024);
+            const uint64_t bd = tc::smem_desc_sw128(kaddr + c * L::kKVChunk + off, 16, 1024);
+            tc::mma_f16(tbase + st * kBlock, ad, bd, idS, kk > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&bars->s_full[st]);        // also frees the K stage
+          if (g > 0 && !pv(g - 1)) {
+            fail(&bars->abort, 7);
+            break;
+          }
+        }
+        if (g == n && !pv(n - 1)) fail(&bars->abort, 8);
+      }
+      // on every path: the products issued so far are done before TMEM is released
+      tc::mma_commit(&bars->drain);
+      tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and epilogue
+    const int q = warp & 3;                  // TMEM lane quarter this warp may access
+    const int r = q * 32 + lane;             // tile row == TMEM lane
+    const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+    const int i = i0 + r / a.G, hq = h * a.G + r % a.G;
+    const bool valid = r < qpt * a.G && i < a.Sq;
+    DenseRow row{0, 0, 0, 0.f};
+    if (valid) row = dense_row(a, seq, b, hq, i);
+    const bool live_warp = __any_sync(0xffffffffu, valid);
+    const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+    const ScoreMap<CAP, BIAS> map(a, row);
+    float mrow = -INFINITY;
+    uint64_t lsum = f2(0.f, 0.f);
+    uint32_t g = 0;
+    bool ok = true;
+    for (int j; (j = walk.next(lane)) >= 0; ++g) {
+      const int sb = g & 1;
+      const uint32_t sp = tbase + lane_off + sb * kBlock;     // S_g, then P_g, of this row
+      if (!warp_wait(&bars->s_full[sb], (g >> 1) & 1, abort)) {
+        fail(&bars->abort, 10);
+        ok = false;
+        break;
+      }
+      if (live_warp) {
+        tc::fence_after_sync();
+        uint32_t sraw[64];
+        {
+          uint32_t (&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sraw[0]);
+          uint32_t (&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sraw[32]);
+          tc::tmem_ld32(sp, lo);
+          tc::tmem_ld32(sp + 32, hi);
+          tc::tmem_ld_wait();
+        }
+        map.template apply<64>(sraw, row.pos - j * kBlock);
+        const uint64_t see = visible64(a, row, doc_k, walk, j);
+        if (__any_sync(0xffffffffu, see != ~0ull)) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (!(((uint32_t)see >> c) & 1u)) sraw[c] = __float_as_uint(-INFINITY);
+            if (!(((uint32_t)(see >> 32) >> c) & 1u)) sraw[32 + c] = __float_as_uint(-INFINITY);
+          }
+        }
+        const float mx = max64(sraw) * map.after;
+        const bool raise = mrow == -INFINITY || mx > mrow + kRescaleLog2;
+        const bool scale_o = raise && g > 0 && mrow != -INFINITY;
+        if (__any_sync(0xffffffffu, scale_o)) {
+          // tcgen05.ld/st are warp-collective: each lane with its own factor (1 where the max stays)
+          const uint32_t gp = g - 1;
+          if (!warp_wait(&bars->pv_done[gp & 1], (gp >> 1) & 1, abort)) {
+            fail(&bars->abort, 12);
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          const float alpha = scale_o ? ex2(mrow - mx) : 1.f;
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tc::tmem_ld32(tbase + lane_off + L::kColO + cc * 32, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st32(tbase + lane_off + L::kColO + cc * 32, o);
+          }
+          tc::tmem_st_wait();
+          float l0, l1;
+          f2_split(lsum, l0, l1);
+          lsum = f2(l0 * alpha, l1 * alpha);
+        }
+        if (raise) mrow = mx;
+        // a row that has seen nothing so far keeps -inf; its weights are exp2(-inf) = 0
+        const float nm = mrow == -INFINITY ? 0.f : -mrow;
+        const uint64_t negm = f2(nm, nm), after2 = f2(map.after, map.after);
+        uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+        uint32_t packed[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const uint64_t x2 = ffma2(f2(__uint_as_float(sraw[2 * c]), __uint_as_float(sraw[2 * c + 1])), after2, negm);
+          float x0, x1;
+          f2_split(x2, x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          acc[c & 3] = fadd2(acc[c & 3], f2(p0, p1));
+          packed[c] = pack_bf16(p0, p1);
+        }
+        lsum = fadd2(lsum, fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])));
+        tc::tmem_st32(sp, packed);           // S_g is in registers
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&bars->p_full[sb]);
+        *reinterpret_cast<volatile int*>(&bars->p_arrived[q]) = (int)g;
+      }
+    }
+    // ------------------------------------------------------------ epilogue
+    if (g > 0 && ok) {
+      if (!warp_wait(&bars->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort)) fail(&bars->abort, 13);
+      tc::fence_after_sync();
+    }
+    const bool broken = __any_sync(0xffffffffu, *abort != 0);
+    if (live_warp) {
+      float l0, l1;
+      f2_split(lsum, l0, l1);
+      const float lrow = l0 + l1;
+      const float nan = __int_as_float(0x7fffffff);
+      const float inv = broken ? nan : (lrow == 0.f ? 0.f : 1.f / lrow);
+      const float lse = broken ? nan : (lrow == 0.f ? -INFINITY : (mrow + log2f(lrow)) * 0.69314718055994531f);
+      const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + i;
+      const int64_t part = (int64_t)split * a.B * a.Hq * a.Sq + flat;
+      const int64_t at = (int64_t)b * a.os.b + (int64_t)hq * a.os.h + (int64_t)i * a.os.s;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;              // no step: a row that sees nothing
+        if (g > 0 && !broken) {
+          tc::tmem_ld32(tbase + lane_off + L::kColO + cc * 32, o);
+          tc::tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+        if (!valid) continue;
+        if (a.splits > 1) {
+          float4* p = reinterpret_cast<float4*>(a.part_o + part * D + cc * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            p[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                               __uint_as_float(o[4 * e + 3]));
+        } else {
+          store_row32(static_cast<__nv_bfloat16*>(a.out) + at + cc * 32,
+                      a.rest != nullptr ? static_cast<__nv_bfloat16*>(a.rest) + at + cc * 32 : nullptr, o);
+        }
+      }
+      if (valid) {
+        if (a.splits > 1)
+          a.part_lse[part] = lse;
+        else if (a.lse != nullptr)
+          a.lse[flat] = lse;
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tbase, L::kTmemCols);
+  if (threadIdx.x == 0 && bars->abort) {
+    // A V copy completes the P barrier of its step only together with the four softmax arrivals;
+    // after an abort the missing ones are made here, and the copies still in flight are waited for.
+    const int va = bars->v_armed;
+    for (int gg = va - 1; gg <= va; ++gg) {
+      if (gg < 0) continue;
+      uint64_t* pb = &bars->p_full[gg & 1];
+      const uint32_t par = ((uint32_t)gg >> 1) & 1;
+      if (tc::mbar_try_wait(pb, par)) continue;
+      for (int w = 0; w < 4; ++w)
+        if (bars->p_arrived[w] < gg) tc::mbar_arrive(pb);
+      tc::mbar_wait_drain(pb, par, kWaitLimit);
+    }
+    if (a.status != nullptr) report_error(a.status, FVATTN_ERR_TIMEOUT, bars->abort);
+  }
+}
+
+template <int D, bool CAP, bool BIAS>
+cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
+  const int qpt = kTileRows / a.G;
+  CUtensorMap mq, mk, mv;
+  if (!make_map_rows(&mq, a.q, a.qs, a, qpt) || !make_map_keys(&mk, a.k, a.ks, a, kBlock) ||
+      !make_map_keys(&mv, a.v, a.vs, a, kBlock))
+    return cudaErrorInvalidValue;
+  const size_t smem = FwdLayout<D>::kBytes + 1024;
+  auto* kernel = dense_tc_kernel<D, CAP, BIAS>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const unsigned tiles = (unsigned)((a.Sq + qpt - 1) / qpt);
+  kernel<<<dim3(tiles * a.splits, a.Hkv, a.B), kWarps * 32, smem, st>>>(mq, mk, mv, a, qpt);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const DenseArgs& a, cudaStream_t st) {
+  const bool cap = a.cap > 0.f, bias = a.mask.slopes != nullptr;
+  if (cap) return bias ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
+  return bias ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_tc(const DenseArgs& a, cudaStream_t st) {
+  return a.d == 128 ? launch_d<128>(a, st) : launch_d<64>(a, st);
+}
+
+}  // namespace fv

@@ -1,0 +1,243 @@
+// Device pieces that the tensor-core kernels of attention over all keys share (forward and backward):
+// bounded waits, the walk over key blocks, masks, the score's cap and bias, and the tensor maps.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "dense.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.cuh"
+
+namespace fv {
+
+constexpr uint32_t kWaitLimit = 1u << 22;    // polls of a bounded wait (seconds, not minutes)
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void fail(int* abort, int code) { atomicCAS(abort, 0, code); }
+
+// A bounded wait taken by a whole warp with one outcome for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  const bool ok = tc::mbar_wait(bar, parity, abort, kWaitLimit);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// 2^x by the ex2.approx instruction (2^-inf = 0), and 1/x by rcp.approx (1/inf = 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Packed pairs of fp32 (one 64-bit register): two operations per instruction.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
+  float m[21];
+#pragma unroll
+  for (int c = 0; c < 21; ++c)
+    m[c] = max3(__uint_as_float(s[3 * c]), __uint_as_float(s[3 * c + 1]), __uint_as_float(s[3 * c + 2]));
+#pragma unroll
+  for (int c = 0; c < 7; ++c) m[c] = max3(m[3 * c], m[3 * c + 1], m[3 * c + 2]);
+  return max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], __uint_as_float(s[63])));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 32 fp32 results as bf16 (and, with rest, what the rounding leaves) to 16-byte aligned memory.
+__device__ __forceinline__ void store_row32(__nv_bfloat16* out, __nv_bfloat16* rest, const uint32_t (&o)[32]) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t w[4], z[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = __uint_as_float(o[8 * v + 2 * e]), y = __uint_as_float(o[8 * v + 2 * e + 1]);
+      w[e] = pack_bf16(x, y);
+      z[e] = pack_bf16(x - __uint_as_float(w[e] << 16), y - __uint_as_float(w[e] & 0xffff0000u));
+    }
+    reinterpret_cast<uint4*>(out)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (rest != nullptr) reinterpret_cast<uint4*>(rest)[v] = make_uint4(z[0], z[1], z[2], z[3]);
+  }
+}
+
+// The documents of the 64-token blocks of a sequence (dense_doc_kernel): x = the lowest number, with the
+// sign bit set when the block has padding tokens too (0x7fffffff without any document); y = the
+// highest (-1 without any).
+__device__ __forceinline__ int doc_low(int2 v) { return v.x & 0x7fffffff; }
+__device__ __forceinline__ bool doc_uniform(int2 v) { return v.x == v.y; }      // one document, no padding
+
+// Ascending walk over the 64-key blocks [j, end) that a set of documents [lo, hi] can see. Used by
+// whole warps: with documents a warp tests 32 blocks at a time.
+struct BlockWalk {
+  const int2* docs;       // null without documents
+  int j, end, lo, hi;
+  uint32_t word;          // blocks of the current window that are left
+  int base;               // its first block; -1 before the first window
+
+  __device__ __forceinline__ BlockWalk(const DenseArgs& a, int b, int begin, int stop, int lo_, int hi_)
+      : docs(nullptr), j(begin), end(stop), lo(lo_), hi(hi_), word(0), base(begin) {
+    if (a.mask.doc_k != nullptr) docs = a.doc_blocks_k + (int64_t)b * ((a.Sk + kBlock - 1) / kBlock);
+  }
+  __device__ __forceinline__ uint32_t window(int at, int lane) const {
+    bool see = false;
+    if (at + lane < end) {
+      const int2 v = docs[at + lane];
+      see = doc_low(v) <= hi && v.y >= lo;
+    }
+    return __ballot_sync(0xffffffffu, see);
+  }
+  __device__ __forceinline__ int next(int lane) {
+    if (docs == nullptr) return j < end ? j++ : -1;
+    while (word == 0) {
+      if (j >= end) return -1;
+      base = j;
+      word = window(j, lane);
+      j += 32;
+    }
+    const int c = __ffs(word) - 1;
+    word &= word - 1;
+    return base + c;
+  }
+  __device__ __forceinline__ int count(int lane) const {
+    if (docs == nullptr) return max(0, end - j);
+    int n = 0;
+    for (int at = j; at < end; at += 32) n += __popc(window(at, lane));
+    return n;
+  }
+};
+
+// Whether block j has keys that do not exist although their memory does.
+__device__ __forceinline__ bool dirty_block(const DenseArgs& a, const DenseSeq& s, int b, int j) {
+  if (s.kv < a.Sk && (j + 1) * kBlock > s.kv) return true;
+  return a.mask.doc_k != nullptr && a.doc_blocks_k[(int64_t)b * ((a.Sk + kBlock - 1) / kBlock) + j].x < 0;
+}
+
+// Bit c: key 64 j + c is visible to the row.
+__device__ __forceinline__ uint64_t visible64(const DenseArgs& a, const DenseRow& row, const int32_t* doc_k,
+                                              const BlockWalk& walk, int j) {
+  const int n = row.limit - j * kBlock;
+  uint64_t see = n >= kBlock ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+  if (doc_k != nullptr) {
+    const int2 v = walk.docs[j];
+    if (doc_uniform(v)) {
+      if (v.y != row.doc) see = 0ull;
+    } else if (see != 0ull) {
+      // bits of keys at or past Sk are clear already: their document numbers are not read
+      uint64_t same = 0ull;
+      for (int c = 0; c < kBlock; ++c)
+        if ((see >> c) & 1ull) same |= (uint64_t)(doc_k[j * kBlock + c] == row.doc) << c;
+      see &= same;
+    }
+  }
+  return see;
+}
+
+// The score of a raw product x, up to the factor `after` that takes it to base-2 exponents:
+// x itself (after = scale log2 e), or the capped and biased score (after = log2 e).
+template <bool CAP, bool BIAS>
+struct ScoreMap {
+  float scale, after, cap, in, slope;
+  __device__ __forceinline__ ScoreMap(const DenseArgs& a, const DenseRow& row) {
+    scale = a.scale;
+    cap = a.cap;
+    after = (CAP || BIAS) ? kLog2e : a.scale * kLog2e;
+    in = CAP ? a.scale / a.cap * (2.f * kLog2e) : 0.f;
+    slope = row.slope;
+  }
+  // tanh(y) = 1 - 2 / (1 + e^2y), off by a few 2^-24 absolutely: with the scaled product that is a few
+  // 2^-24 of the cap. e^2y overflowing to inf or vanishing gives 1 and -1.
+  __device__ __forceinline__ float tanh_of(float x) const { return fmaf(-2.f, rcp(1.f + ex2(x * in)), 1.f); }
+  // N scores in place; `far` = position of the row minus the first key.
+  template <int N>
+  __device__ __forceinline__ void apply(uint32_t (&s)[N], int far) const {
+    if (!CAP && !BIAS) return;
+    const float f = (float)far;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      float x = __uint_as_float(s[c]);
+      x = CAP ? cap * tanh_of(x) : x * scale;
+      if (BIAS) x = fmaf(-slope, fabsf(f - (float)c), x);
+      s[c] = __float_as_uint(x);
+    }
+  }
+};
+
+// `rows` tokens from token t0 of a [token][D] matrix into a tile of 128-byte swizzled rows (chunks of 64
+// dims), zeros for tokens at or past `end` and for padding documents; lanes `me` of `of`.
+template <int D>
+__device__ __forceinline__ void copy_keys(unsigned char* dst, const __nv_bfloat16* base, int64_t stride, int t0, int rows,
+                                          int end, const int32_t* doc, int me, int of) {
+  for (int x = me; x < rows * (D / 8); x += of) {
+    const int r = x / (D / 8), c = x % (D / 8);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (t0 + r < end && (doc == nullptr || doc[t0 + r] >= 0))
+      v = *reinterpret_cast<const uint4*>(base + (int64_t)(t0 + r) * stride + c * 8);
+    *reinterpret_cast<uint4*>(dst + (c / 8) * rows * 128 + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v;
+  }
+}
+
+// ------------------------------------------------------------------ tensor maps (host)
+
+inline bool encode_bf16(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const int64_t* strides,
+                        const cuuint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t bytes[4];
+  for (int i = 0; i < rank - 1; ++i) bytes[i] = (cuuint64_t)strides[i] * 2;
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, bytes, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [B][Hq][Sq][d] seen as [B][Hkv][Sq][G][d], read in boxes of `queries` queries of all G heads and 64
+// dims: row i * G + g of the box is query i of head g. Queries past Sq read as zeros.
+inline bool make_map_rows(CUtensorMap* map, const void* base, const fvattn_strides& s, const DenseArgs& a, int queries) {
+  const cuuint64_t dims[5] = {(cuuint64_t)a.d, (cuuint64_t)a.G, (cuuint64_t)a.Sq, (cuuint64_t)a.Hkv, (cuuint64_t)a.B};
+  const int64_t strides[4] = {s.h, s.s, s.h * a.G, s.b};
+  const cuuint32_t box[5] = {64, (cuuint32_t)a.G, (cuuint32_t)queries, 1, 1};
+  return encode_bf16(map, base, 5, dims, strides, box);
+}
+
+// [B][Hkv][Sk][d], read in boxes of `keys` keys and 64 dims; keys past Sk read as zeros.
+inline bool make_map_keys(CUtensorMap* map, const void* base, const fvattn_strides& s, const DenseArgs& a, int keys) {
+  const cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.Sk, (cuuint64_t)a.Hkv, (cuuint64_t)a.B};
+  const int64_t strides[3] = {s.s, s.h, s.b};
+  const cuuint32_t box[4] = {64, (cuuint32_t)keys, 1, 1};
+  return encode_bf16(map, base, 4, dims, strides, box);
+}
+
+}  // namespace fv
