@@ -142,8 +142,7 @@ struct DenseWs {
   size_t part_o, part_lse, delta, docs_q, docs_k, total;
 };
 
-bool uses_tc(const DenseArgs&, int dtype) { return dtype == FVATTN_BF16; }
-size_t doc_bytes(int64_t B, int64_t S) { return (size_t)(B * ((S + kBlock - 1) / kBlock)) * sizeof(int2); }
+size_t doc_bytes(int64_t B, int64_t S, int64_t block) { return (size_t)(B * ((S + block - 1) / block)) * sizeof(int2); }
 
 DenseWs fwd_ws(const DenseArgs& a, int dtype) {
   DenseWs w{};
@@ -153,15 +152,21 @@ DenseWs fwd_ws(const DenseArgs& a, int dtype) {
     w.part_o = take(off, rows * a.splits * a.d * sizeof(float));
     w.part_lse = take(off, rows * a.splits * sizeof(float));
   }
-  if (uses_tc(a, dtype) && a.mask.doc_k != nullptr) w.docs_k = take(off, doc_bytes(a.B, a.Sk));
+  if (dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) w.docs_k = take(off, doc_bytes(a.B, a.Sk, kBlock));
   w.total = off;
   return w;
 }
 
-DenseWs bwd_ws(const DenseArgs& a) {
+constexpr int kBwdKeys = 128;      // keys of a tile of the gradients' kernels
+
+DenseWs bwd_ws(const DenseArgs& a, int dtype) {
   DenseWs w{};
   size_t off = 0;
   w.delta = take(off, (size_t)a.B * a.Hq * a.Sq * sizeof(float));
+  if (dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
+    w.docs_q = take(off, doc_bytes(a.B, a.Sq, kTileRows / a.G));
+    w.docs_k = take(off, doc_bytes(a.B, a.Sk, kBwdKeys));
+  }
   w.total = off;
   return w;
 }
@@ -173,10 +178,6 @@ DenseArgs fwd_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
 }
 
 }  // namespace
-
-namespace fv {
-cudaError_t launch_dense_simple_bf16_bwd(const DenseArgs& a, cudaStream_t st);
-}  // namespace fv
 
 extern "C" {
 
@@ -276,18 +277,18 @@ int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (uses_tc(a, shape->dtype) && a.mask.doc_k != nullptr) {
+  if (shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
     a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
-    e = launch_dense_docs(a, false, s);
+    e = launch_dense_docs(a.mask.doc_k, a.doc_blocks_k, a.B, a.Sk, kBlock, s);
   }
-  if (e == cudaSuccess) e = uses_tc(a, shape->dtype) ? launch_dense_tc(a, s) : launch_dense_f32(a, s);
+  if (e == cudaSuccess) e = shape->dtype == FVATTN_BF16 ? launch_dense_tc(a, s) : launch_dense_f32(a, s);
   if (e == cudaSuccess && a.splits > 1) e = launch_dense_combine(a, shape->dtype, s);
   return cuda_status(e);
 }
 
 size_t fvattn_dense_attn_bwd_workspace_bytes(const fvattn_dense_shape* shape, const fvattn_dense_mask* mask) {
   if (validate_dense(shape, mask, true) != FVATTN_OK) return (size_t)-1;
-  return bwd_ws(dense_args(shape, mask)).total;
+  return bwd_ws(dense_args(shape, mask), shape->dtype).total;
 }
 
 int fvattn_dense_attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out,
@@ -302,7 +303,7 @@ int fvattn_dense_attn_bwd(const void* dout, const void* q, const void* k, const 
   if (!aligned(lse, 4) || !aligned(status, 4)) return FVATTN_ERR_INVALID;
   if (rest != nullptr && shape->dtype != FVATTN_BF16) return FVATTN_ERR_INVALID;
   DenseArgs a = dense_args(shape, mask);
-  const DenseWs w = bwd_ws(a);
+  const DenseWs w = bwd_ws(a, shape->dtype);
   if (workspace == nullptr || !aligned(workspace, 256)) return FVATTN_ERR_INVALID;
   if (workspace_bytes < w.total) return FVATTN_ERR_CAPACITY;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -320,8 +321,13 @@ int fvattn_dense_attn_bwd(const void* dout, const void* q, const void* k, const 
   a.status = status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_dense_delta(a, shape->dtype, s);
-  if (e == cudaSuccess)
-    e = shape->dtype == FVATTN_F32 ? launch_dense_f32_bwd(a, s) : launch_dense_simple_bf16_bwd(a, s);
+  if (e == cudaSuccess && shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
+    a.doc_blocks_q = reinterpret_cast<int2*>(ws + w.docs_q);
+    a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
+    e = launch_dense_docs(a.mask.doc_q, a.doc_blocks_q, a.B, a.Sq, kTileRows / a.G, s);
+    if (e == cudaSuccess) e = launch_dense_docs(a.mask.doc_k, a.doc_blocks_k, a.B, a.Sk, kBwdKeys, s);
+  }
+  if (e == cudaSuccess) e = shape->dtype == FVATTN_BF16 ? launch_dense_bwd_tc(a, s) : launch_dense_f32_bwd(a, s);
   return cuda_status(e);
 }
 

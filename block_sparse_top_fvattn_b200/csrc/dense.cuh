@@ -29,7 +29,9 @@ struct DenseArgs {
   int splits, split_keys;         // forward: the keys in `splits` ranges of split_keys (a multiple of 64)
   float *part_o, *part_lse;       // splits > 1: [splits][B][Hq][Sq][d] and [splits][B][Hq][Sq]
   float* delta;                   // backward: [B][Hq][Sq], sum_d out * dout
-  int2 *doc_blocks_q, *doc_blocks_k;   // documents of the 64-token blocks (dense_doc_kernel)
+  // Documents of blocks of tokens (dense_doc_kernel), null without documents: of the keys in blocks of
+  // 64 (forward) or 128 (backward), of the queries in row tiles (backward).
+  int2 *doc_blocks_q, *doc_blocks_k;
   int32_t* status;
 };
 
@@ -77,7 +79,8 @@ __device__ __forceinline__ DenseRow dense_row(const DenseArgs& a, const DenseSeq
 }
 
 // Launchers. Each returns the launch's error.
-cudaError_t launch_dense_docs(const DenseArgs& a, bool queries, cudaStream_t st);
+cudaError_t launch_dense_docs(const int32_t* doc, int2* blocks, int B, int S, int block, cudaStream_t st);
+cudaError_t launch_dense_bwd_tc(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_tc(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_f32(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st);

@@ -1,0 +1,798 @@
+// Gradients of attention over all keys on the B200 tensor cores: bf16 inputs, everything else fp32.
+//
+//   P = exp(s - lse),  dP = dout V^T,  dS = P (dP - delta) (1 - tanh^2)
+//   dV = P^T dout,  dK = scale dS^T Q,  dQ = scale dS K,  delta_i = sum_d out_id dout_id
+//
+// Two kernels, each of which owns its results: one CTA per 128 keys walks over the row tiles (row
+// i * G + g: query i of the group's head g) and keeps dK and dV in TMEM, one CTA per row tile walks over the keys
+// and keeps dQ. S and dP are made twice (seven products instead of five), but no result is added to
+// by several CTAs, so there are no atomics, equal calls give equal bits, and a shared key head's
+// gradient is summed over its query heads in TMEM.
+//
+// dK, dV: scores transposed (lane = key, column = row), so that P^T and dS^T are written over the
+// scores in TMEM as the first operands of their products. Per tile, with eight warps between them:
+//   products   dV(i) S(i+1)            | dK(i) dP(i+1)
+//   warps      dS(i) from dP(i), P(i)  | P(i+1) from S(i+1)
+// dQ: lane = row; S has two buffers, so S(i+1) is ready when dS(i) is done:
+//   products   dP(i+1) dQ(i) S(i+2);   warps   P(i+1), then dS(i+1) from dP(i+1)
+//
+// P and dS are rounded to bf16 as the products' operands; lse, delta and all sums stay in fp32, and
+// the scale is applied once to the sums.
+//
+// Every wait is bounded; one that runs out stops every role without leaving a copy or product in
+// flight, is reported in the status word, and makes the CTA's results NaN.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "dense.cuh"
+#include "dense_tc.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.cuh"
+
+namespace fv {
+
+namespace {
+
+constexpr int kT = 128;               // rows and keys of a tile
+constexpr int kWarps = 10;            // loader, MMA, eight for the elementwise work
+constexpr int kThreads = kWarps * 32;
+constexpr uint32_t kColA = 0;         // scores (dQ: their first buffer)
+constexpr uint32_t kColB = 128;       // dP (dQ: the scores' second buffer)
+
+template <int D>
+struct BwdLayout {
+  static constexpr int kChunk = kT * 128;              // [128 tokens x 64 dims] bf16
+  static constexpr int kTile = (D / 64) * kChunk;
+};
+
+// A token-by-dims tile as the K-major operand of a product over dims, and as the MN-major second operand
+// of a product over tokens.
+__device__ __forceinline__ uint64_t desc_dims(uint32_t addr, int kk) {
+  return tc::smem_desc_sw128(addr + (kk >> 2) * (kT * 128) + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t desc_tokens(uint32_t addr, int kk) {
+  return tc::smem_desc_sw128(addr + kk * 16 * 128, kT * 128, 1024);
+}
+
+// D[128 x 128] = A B^T over the dims of two tiles.
+template <int D>
+__device__ __forceinline__ void mma_dims(uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr) {
+  constexpr uint32_t id = tc::idesc_bf16_f32(kT, kT, 0, 0);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) tc::mma_f16(d_tmem, desc_dims(a_addr, kk), desc_dims(b_addr, kk), id, kk > 0);
+}
+// D[128 x D] (+)= W B over the 128 tokens of a tile, W (bf16) in TMEM: the first 64 tokens at w, the
+// others 64 columns further, each half over the fp32 values it was made from.
+template <int D>
+__device__ __forceinline__ void mma_tokens(uint32_t d_tmem, uint32_t w, uint32_t b_addr, bool add) {
+  constexpr uint32_t id = tc::idesc_bf16_f32(kT, D, 0, 1);
+#pragma unroll
+  for (int kk = 0; kk < kT / 16; ++kk)
+    tc::mma_f16_tmem_a(d_tmem, w + (kk >> 2) * 64 + (kk & 3) * 8, desc_tokens(b_addr, kk), id, add || kk > 0);
+}
+
+// 32 fp32 results, times `by`, as bf16.
+__device__ __forceinline__ void store32(__nv_bfloat16* p, uint32_t (&o)[32], float by) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+  store_row32(p, nullptr, o);
+}
+
+// ------------------------------------------------------------------ dK, dV
+
+// What a row tile's rows need, per stage.
+struct RowStats {
+  float lse2[kT];      // lse log2 e
+  float delta[kT];
+  float far[kT];       // position minus the first key of the key tile
+  float slope2[kT];    // slope log2 e
+  int limit[kT];       // visible keys are below it, counted from the first key of the key tile
+  int doc[kT];
+};
+
+template <int D>
+struct DkvLayout : BwdLayout<D> {
+  using B = BwdLayout<D>;
+  static constexpr int kOffK = 0, kOffV = B::kTile, kOffQ = 2 * B::kTile, kOffG = 4 * B::kTile;
+  static constexpr int kOffStats = 6 * B::kTile;
+  static constexpr int kOffBar = kOffStats + 2 * (int)sizeof(RowStats);
+  static constexpr int kBytes = kOffBar + 256;
+  static constexpr uint32_t kColV = 256, kColK = 384;
+};
+
+struct DkvBars {
+  uint64_t kv_full;
+  uint64_t q_full[2], q_empty[2];     // Q and the row statistics of a tile
+  uint64_t g_full[2], g_empty[2];     // dout of a tile
+  uint64_t s_full, p_full, dp_full, ds_full;
+  uint64_t drain;
+  int masked[2];                      // whether some pair of the tile is not visible
+  int doc_lo, doc_hi, doc_pad;        // documents of the keys
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const DenseArgs a, const int qpt) {
+  using L = DkvLayout<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  DkvBars* bars = reinterpret_cast<DkvBars*>(smem + L::kOffBar);
+  RowStats* stats = reinterpret_cast<RowStats*>(smem + L::kOffStats);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &bars->abort;
+  const int h = blockIdx.y, b = blockIdx.z, j0 = blockIdx.x * kT;
+  const DenseSeq seq = dense_seq(a, b);
+  const int32_t* doc_q = a.mask.doc_q != nullptr ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
+  const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+  const int tiles = (a.Sq + qpt - 1) / qpt;
+
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->kv_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&bars->q_full[s], 2);      // the copy (or its stand-in), the statistics
+      tc::mbar_init(&bars->q_empty[s], 1);
+      tc::mbar_init(&bars->g_full[s], 1);
+      tc::mbar_init(&bars->g_empty[s], 1);
+    }
+    tc::mbar_init(&bars->s_full, 1);
+    tc::mbar_init(&bars->dp_full, 1);
+    tc::mbar_init(&bars->p_full, 8);
+    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    bars->doc_lo = 0x7fffffff;
+    bars->doc_hi = -1;
+    bars->doc_pad = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&bars->tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  // Rows that no copy writes (128 - qpt * G of them) have weights of zero: they must hold numbers.
+  if (qpt * a.G < kT) {
+    for (int x = threadIdx.x; x < 4 * L::kTile / 16; x += kThreads)
+      reinterpret_cast<uint4*>(smem + L::kOffQ)[x] = make_uint4(0u, 0u, 0u, 0u);
+    tc::fence_proxy_async_smem();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (doc_k != nullptr) {
+    if (threadIdx.x < kT && j0 + threadIdx.x < a.Sk) {
+      const int doc = doc_k[j0 + threadIdx.x];
+      if (doc >= 0) {
+        atomicMin(&bars->doc_lo, doc);
+        atomicMax(&bars->doc_hi, doc);
+      } else {
+        bars->doc_pad = 1;
+      }
+    }
+    __syncthreads();
+  }
+  const uint32_t tbase = bars->tmem_base;
+  // Under an order the rows from the first whose limit passes j0 see the tile (limits never fall).
+  int first = 0;
+  if (j0 >= seq.kv) {
+    first = tiles;
+  } else if (a.causal && j0 >= seq.prefix) {
+    first = max(0, min(j0 - seq.q0, a.Sq)) / qpt;      // query i sees key j0 when q0 + i >= j0
+  }
+  BlockWalk walk(a.doc_blocks_q != nullptr ? a.doc_blocks_q + (int64_t)b * tiles : nullptr, first, tiles, bars->doc_lo,
+                bars->doc_hi);
+  const uint32_t n = (uint32_t)walk.count(lane);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loader
+    bool kv_armed = false;
+    int q_par[2] = {-1, -1}, g_par[2] = {-1, -1};
+    if (lane == 0 && n > 0) {
+      tc::mbar_expect_tx(&bars->kv_full, 2 * L::kTile);
+      kv_armed = true;
+      for (int c = 0; c < D / 64; ++c) {
+        tc::tma_load_4d(smem + L::kOffK + c * L::kChunk, &tmK, &bars->kv_full, c * 64, j0, h, b);
+        tc::tma_load_4d(smem + L::kOffV + c * L::kChunk, &tmV, &bars->kv_full, c * 64, j0, h, b);
+      }
+    }
+    const uint32_t bytes = (uint32_t)(qpt * a.G) * 128 * (D / 64);
+    const int jend = min(kT, seq.kv - j0);
+    uint32_t g = 0;
+    for (int t; (t = walk.next(lane)) >= 0; ++g) {
+      const int s = g & 1;
+      const uint32_t par = (g >> 1) & 1;
+      const int i0 = t * qpt;
+      // padding queries may hold anything: their tiles are copied by hand, with zeros for them
+      const bool pad = doc_q != nullptr && a.doc_blocks_q[(int64_t)b * tiles + t].x < 0;
+      unsigned char *sq = smem + L::kOffQ + s * L::kTile, *sg = smem + L::kOffG + s * L::kTile;
+      if (!warp_wait(&bars->q_empty[s], par ^ 1, abort)) {
+        fail(&bars->abort, 3);
+        break;
+      }
+      if (!pad) {
+        if (lane == 0) {
+          tc::mbar_expect_tx(&bars->q_full[s], bytes);
+          for (int c = 0; c < D / 64; ++c)
+            tc::tma_load_5d(sq + c * L::kChunk, &tmQ, &bars->q_full[s], c * 64, 0, i0, h, b);
+        }
+      } else {
+        copy_rows<D>(sq, static_cast<const __nv_bfloat16*>(a.q), a.qs, a, b, h, i0, qpt, doc_q, lane, 32);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->q_full[s]);
+      }
+      q_par[s] = (int)par;
+      // row statistics
+      RowStats& st = stats[s];
+      bool full = true;
+#pragma unroll
+      for (int u = 0; u < kT / 32; ++u) {
+        const int r = u * 32 + lane, i = i0 + r / a.G;
+        DenseRow row{0, -1, 0, 0.f};
+        float lse = 0.f, delta = 0.f;
+        if (r < qpt * a.G && i < a.Sq) {
+          const int hq = h * a.G + r % a.G;
+          row = dense_row(a, seq, b, hq, i);
+          const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + i;
+          lse = a.lse[flat];
+          delta = a.delta[flat];
+        }
+        st.lse2[r] = lse * kLog2e;
+        st.delta[r] = delta;
+        st.far[r] = (float)(row.pos - j0);
+        st.slope2[r] = row.slope * kLog2e;
+        st.limit[r] = row.limit - j0;
+        st.doc[r] = row.doc;
+        full = full && row.limit - j0 >= jend && (doc_q == nullptr || (row.doc == bars->doc_lo));
+      }
+      full = __all_sync(0xffffffffu, full);
+      if (lane == 0) {
+        // keys that do not exist need no mask here: they reach only their own results, written as zeros
+        bars->masked[s] = !(full && (doc_k == nullptr || (bars->doc_lo == bars->doc_hi && !bars->doc_pad)));
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->q_full[s]);
+      if (!warp_wait(&bars->g_empty[s], par ^ 1, abort)) {
+        fail(&bars->abort, 4);
+        break;
+      }
+      if (!pad) {
+        if (lane == 0) {
+          tc::mbar_expect_tx(&bars->g_full[s], bytes);
+          for (int c = 0; c < D / 64; ++c)
+            tc::tma_load_5d(sg + c * L::kChunk, &tmG, &bars->g_full[s], c * 64, 0, i0, h, b);
+        }
+      } else {
+        copy_rows<D>(sg, static_cast<const __nv_bfloat16*>(a.dout), a.dos, a, b, h, i0, qpt, doc_q, lane, 32);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->g_full[s]);
+      }
+      g_par[s] = (int)par;
+    }
+    if (lane == 0) {
+      // no copy may still be writing shared memory when the CTA leaves
+      if (kv_armed) tc::mbar_wait_drain(&bars->kv_full, 0, kWaitLimit);
+      for (int s = 0; s < 2; ++s) {
+        if (q_par[s] >= 0) tc::mbar_wait_drain(&bars->q_full[s], (uint32_t)q_par[s], kWaitLimit);
+        if (g_par[s] >= 0) tc::mbar_wait_drain(&bars->g_full[s], (uint32_t)g_par[s], kWaitLimit);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && n > 0) {
+      const uint32_t ka = tc::smem_u32(smem + L::kOffK), va = tc::smem_u32(smem + L::kOffV);
+      const uint32_t qa = tc::smem_u32(smem + L::kOffQ), ga = tc::smem_u32(smem + L::kOffG);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+        if (ok && !tc::mbar_wait(bar, parity, abort, kWaitLimit)) {
+          fail(&bars->abort, code);
+          ok = false;
+        }
+        tc::fence_after_sync();
+        return ok;
+      };
+      auto scores = [&](uint32_t g) {
+        if (!wait(&bars->q_full[g & 1], (g >> 1) & 1, 5)) return;
+        mma_dims<D>(tbase + kColA, ka, qa + (g & 1) * L::kTile);
+        tc::mma_commit(&bars->s_full);
+      };
+      auto dprobs = [&](uint32_t g) {
+        if (!wait(&bars->g_full[g & 1], (g >> 1) & 1, 6)) return;
+        mma_dims<D>(tbase + kColB, va, ga + (g & 1) * L::kTile);
+        tc::mma_commit(&bars->dp_full);
+      };
+      wait(&bars->kv_full, 0, 7);
+      if (ok) scores(0);
+      if (ok) dprobs(0);
+      for (uint32_t g = 0; ok && g < n; ++g) {
+        if (!wait(&bars->p_full, g & 1, 8)) break;
+        mma_tokens<D>(tbase + L::kColV, tbase + kColA, ga + (g & 1) * L::kTile, g > 0);
+        tc::mma_commit(&bars->g_empty[g & 1]);
+        if (g + 1 < n) scores(g + 1);
+        if (!wait(&bars->ds_full, g & 1, 9)) break;
+        mma_tokens<D>(tbase + L::kColK, tbase + kColB, qa + (g & 1) * L::kTile, g > 0);
+        tc::mma_commit(&bars->q_empty[g & 1]);
+        if (g + 1 < n) dprobs(g + 1);
+      }
+      // on every path: the products issued so far are done before TMEM is read or released
+      tc::mma_commit(&bars->drain);
+      tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+    }
+  } else {
+    // ------------------------------------------------------------ elementwise
+    const int q = warp & 3, half = (warp - 2) >> 2;      // TMEM lane quarter; first or second 64 rows of a tile
+    const int r = q * 32 + lane, j = j0 + r;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const uint32_t colS = tbase + lanes + kColA + half * 64, colP = tbase + lanes + kColB + half * 64;
+    const int my_doc = doc_k != nullptr && j < a.Sk ? doc_k[j] : 0;
+    const bool key_ok = j < seq.kv && my_doc >= 0;
+    const float cap2 = a.cap * kLog2e, in = CAP ? a.scale / a.cap * (2.f * kLog2e) : 0.f, scale2 = a.scale * kLog2e;
+    const float fr = (float)r;
+    bool ok = true;
+    for (uint32_t g = 0; g < n; ++g) {
+      const RowStats& st = stats[g & 1];
+      if (!warp_wait(&bars->q_full[g & 1], (g >> 1) & 1, abort) || !warp_wait(&bars->s_full, g & 1, abort)) {
+        fail(&bars->abort, 10);
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      // pw: P, then P times the cap's derivative
+      float pw[64];
+      uint64_t see = ~0ull;
+      if (bars->masked[g & 1]) {
+        see = 0ull;
+        if (key_ok) {
+#pragma unroll 8
+          for (int c = 0; c < 64; ++c) {
+            const int cc = half * 64 + c;
+            const bool v = r < st.limit[cc] && (doc_k == nullptr || st.doc[cc] == my_doc);
+            see |= (uint64_t)v << c;
+          }
+        }
+      }
+#pragma unroll
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        uint32_t s[32], packed[16];
+        tc::tmem_ld32(colS + c0, s);
+        tc::tmem_ld_wait();
+        const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const int at = half * 64 + c0 + c;
+          const float4 l4 = *reinterpret_cast<const float4*>(&st.lse2[at]);
+          const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+          float f[4], sl[4];
+          if (BIAS) {
+            const float4 f4 = *reinterpret_cast<const float4*>(&st.far[at]);
+            const float4 s4 = *reinterpret_cast<const float4*>(&st.slope2[at]);
+            f[0] = f4.x; f[1] = f4.y; f[2] = f4.z; f[3] = f4.w;
+            sl[0] = s4.x; sl[1] = s4.y; sl[2] = s4.z; sl[3] = s4.w;
+          }
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __uint_as_float(s[c + e]);
+            float y, dcap = 1.f;
+            if (CAP) {
+              const float t = fmaf(-2.f, rcp(1.f + ex2(x * in)), 1.f);
+              y = fmaf(cap2, t, -l[e]);
+              dcap = fmaf(-t, t, 1.f);
+            } else {
+              y = fmaf(x, scale2, -l[e]);
+            }
+            if (BIAS) y = fmaf(-sl[e], fabsf(f[e] - fr), y);
+            p[e] = (bits >> (c + e)) & 1u ? ex2(y) : 0.f;
+            pw[c0 + c + e] = CAP ? p[e] * dcap : p[e];
+          }
+          packed[c / 2] = pack_bf16(p[0], p[1]);
+          packed[c / 2 + 1] = pack_bf16(p[2], p[3]);
+        }
+        // P^T over the scores it was made from: columns 0-31 of this half, all of them loaded by now
+        tc::tmem_st16(colS + c0 / 2, packed);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->p_full);
+      if (!warp_wait(&bars->dp_full, g & 1, abort)) {
+        fail(&bars->abort, 11);
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+#pragma unroll
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        uint32_t dp[32], packed[16];
+        tc::tmem_ld32(colP + c0, dp);
+        tc::tmem_ld_wait();
+        const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 d4 = *reinterpret_cast<const float4*>(&st.delta[half * 64 + c0 + c]);
+          const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+          float ds[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ds[e] = pw[c0 + c + e] * (__uint_as_float(dp[c + e]) - d[e]);
+            if (!((bits >> (c + e)) & 1u)) ds[e] = 0.f;       // dP of a masked pair may be anything
+          }
+          packed[c / 2] = pack_bf16(ds[0], ds[1]);
+          packed[c / 2 + 1] = pack_bf16(ds[2], ds[3]);
+        }
+        tc::tmem_st16(colP + c0 / 2, packed);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+    }
+    // ------------------------------------------------------------ results: one half writes dV, the other dK
+    if (n > 0 && ok) {
+      if (!warp_wait(&bars->drain, 0, abort)) fail(&bars->abort, 12);
+      tc::fence_after_sync();
+    }
+    const bool broken = __any_sync(0xffffffffu, *abort != 0);
+    const float by = broken ? __int_as_float(0x7fffffff) : half == 0 ? 1.f : a.scale;
+    const fvattn_strides& ss = half == 0 ? a.dvs : a.dks;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(half == 0 ? a.dv : a.dk) + (int64_t)b * ss.b + (int64_t)h * ss.h +
+                         (int64_t)j * ss.s;
+#pragma unroll 1
+    for (int cc = 0; cc < D / 32; ++cc) {
+      uint32_t o[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = 0u;
+      if (n > 0 && !broken) {
+        tc::tmem_ld32(tbase + lanes + (half == 0 ? L::kColV : L::kColK) + cc * 32, o);
+        tc::tmem_ld_wait();
+      }
+      if (!key_ok && !broken) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+      if (j < a.Sk) store32(dst + cc * 32, o, by);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tbase, 512);
+  if (threadIdx.x == 0 && bars->abort && a.status != nullptr)
+    report_error(a.status, FVATTN_ERR_TIMEOUT, 300 + bars->abort);
+}
+
+// ------------------------------------------------------------------ dQ
+
+template <int D>
+struct DqLayout : BwdLayout<D> {
+  using B = BwdLayout<D>;
+  static constexpr int kStagesK = 3, kStagesV = 2;
+  static constexpr int kOffQ = 0, kOffG = B::kTile, kOffK = 2 * B::kTile, kOffV = kOffK + kStagesK * B::kTile;
+  static constexpr int kOffBar = kOffV + kStagesV * B::kTile;
+  static constexpr int kBytes = kOffBar + 256;
+  static constexpr uint32_t kColDp = 256, kColQ = 384;
+};
+
+struct DqBars {
+  uint64_t q_full;
+  uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+  uint64_t s_full[2], dp_full, ds_full;
+  uint64_t drain;
+  int doc_lo, doc_hi;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const DenseArgs a, const int qpt) {
+  using L = DqLayout<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  DqBars* bars = reinterpret_cast<DqBars*>(smem + L::kOffBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &bars->abort;
+  const int t = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;      // the longest tiles first
+  const int i0 = t * qpt, i1 = min(i0 + qpt, a.Sq);
+  const DenseSeq seq = dense_seq(a, b);
+  const int32_t* doc_q = a.mask.doc_q != nullptr ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
+  const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+  const int blocks = (a.Sk + kT - 1) / kT;
+
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->q_full, 1);
+    for (int s = 0; s < 3; ++s) {
+      tc::mbar_init(&bars->k_full[s], 1);
+      tc::mbar_init(&bars->k_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&bars->v_full[s], 1);
+      tc::mbar_init(&bars->v_empty[s], 1);
+      tc::mbar_init(&bars->s_full[s], 1);
+    }
+    tc::mbar_init(&bars->dp_full, 1);
+    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    bars->doc_lo = 0x7fffffff;
+    bars->doc_hi = -1;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&bars->tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (doc_q != nullptr) {
+    for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
+      const int doc = doc_q[i];
+      if (doc >= 0) {
+        atomicMin(&bars->doc_lo, doc);
+        atomicMax(&bars->doc_hi, doc);
+      }
+    }
+    __syncthreads();
+  }
+  const uint32_t tbase = bars->tmem_base;
+  const int key1 = dense_limit(seq, a.causal, i1 - 1);
+  BlockWalk walk(a.doc_blocks_k != nullptr ? a.doc_blocks_k + (int64_t)b * blocks : nullptr, 0, (key1 + kT - 1) / kT,
+                 bars->doc_lo, bars->doc_hi);
+  const uint32_t n = (uint32_t)walk.count(lane);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loader
+    bool q_armed = false;
+    int k_par[3] = {-1, -1, -1}, v_par[2] = {-1, -1};
+    if (lane == 0 && n > 0) {
+      tc::mbar_expect_tx(&bars->q_full, 2 * (uint32_t)(qpt * a.G) * 128 * (D / 64));
+      q_armed = true;
+      for (int c = 0; c < D / 64; ++c) {
+        tc::tma_load_5d(smem + L::kOffQ + c * L::kChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
+        tc::tma_load_5d(smem + L::kOffG + c * L::kChunk, &tmG, &bars->q_full, c * 64, 0, i0, h, b);
+      }
+    }
+    uint32_t g = 0;
+    for (int j; (j = walk.next(lane)) >= 0; ++g) {
+      const int sk = g % 3, sv = g & 1;
+      const uint32_t pk = (g / 3) & 1, pv = (g >> 1) & 1;
+      unsigned char* dk = smem + L::kOffK + sk * L::kTile;
+      if (!warp_wait(&bars->k_empty[sk], pk ^ 1, abort)) {
+        fail(&bars->abort, 3);
+        break;
+      }
+      // keys that do not exist: zeros, whatever their memory holds (0 * NaN would reach dQ)
+      const bool dirty = (seq.kv < a.Sk && (j + 1) * kT > seq.kv) || (doc_k != nullptr && walk.docs[j].x < 0);
+      if (dirty) {
+        copy_keys<D>(dk, static_cast<const __nv_bfloat16*>(a.k) + (int64_t)b * a.ks.b + (int64_t)h * a.ks.h, a.ks.s, j * kT,
+                     kT, seq.kv, doc_k, lane, 32);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->k_full[sk]);
+      } else if (lane == 0) {
+        tc::mbar_expect_tx(&bars->k_full[sk], L::kTile);
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_4d(dk + c * L::kChunk, &tmK, &bars->k_full[sk], c * 64, j * kT, h, b);
+      }
+      k_par[0] = sk == 0 ? (int)pk : k_par[0];
+      k_par[1] = sk == 1 ? (int)pk : k_par[1];
+      k_par[2] = sk == 2 ? (int)pk : k_par[2];
+      if (!warp_wait(&bars->v_empty[sv], pv ^ 1, abort)) {
+        fail(&bars->abort, 4);
+        break;
+      }
+      if (lane == 0) {
+        tc::mbar_expect_tx(&bars->v_full[sv], L::kTile);
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_4d(smem + L::kOffV + sv * L::kTile + c * L::kChunk, &tmV, &bars->v_full[sv], c * 64, j * kT, h, b);
+      }
+      v_par[0] = sv == 0 ? (int)pv : v_par[0];
+      v_par[1] = sv == 1 ? (int)pv : v_par[1];
+    }
+    if (lane == 0) {
+      if (q_armed) tc::mbar_wait_drain(&bars->q_full, 0, kWaitLimit);
+#pragma unroll
+      for (int s = 0; s < 3; ++s)
+        if (k_par[s] >= 0) tc::mbar_wait_drain(&bars->k_full[s], (uint32_t)k_par[s], kWaitLimit);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (v_par[s] >= 0) tc::mbar_wait_drain(&bars->v_full[s], (uint32_t)v_par[s], kWaitLimit);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && n > 0) {
+      const uint32_t qa = tc::smem_u32(smem + L::kOffQ), ga = tc::smem_u32(smem + L::kOffG);
+      const uint32_t ka = tc::smem_u32(smem + L::kOffK), va = tc::smem_u32(smem + L::kOffV);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+        if (ok && !tc::mbar_wait(bar, parity, abort, kWaitLimit)) {
+          fail(&bars->abort, code);
+          ok = false;
+        }
+        tc::fence_after_sync();
+        return ok;
+      };
+      auto scores = [&](uint32_t g) {
+        if (!wait(&bars->k_full[g % 3], (g / 3) & 1, 5)) return;
+        mma_dims<D>(tbase + (g & 1 ? kColB : kColA), qa, ka + (g % 3) * L::kTile);
+        tc::mma_commit(&bars->s_full[g & 1]);
+      };
+      auto dprobs = [&](uint32_t g) {
+        if (!wait(&bars->v_full[g & 1], (g >> 1) & 1, 6)) return;
+        mma_dims<D>(tbase + L::kColDp, ga, va + (g & 1) * L::kTile);
+        tc::mma_commit(&bars->dp_full);
+        tc::mma_commit(&bars->v_empty[g & 1]);
+      };
+      wait(&bars->q_full, 0, 7);
+      if (ok) scores(0);
+      if (ok) dprobs(0);
+      for (uint32_t g = 0; ok && g < n; ++g) {
+        if (g + 1 < n) scores(g + 1);
+        if (!wait(&bars->ds_full, g & 1, 8)) break;
+        if (g + 1 < n) dprobs(g + 1);
+        if (!ok) break;
+        mma_tokens<D>(tbase + L::kColQ, tbase + (g & 1 ? kColB : kColA), ka + (g % 3) * L::kTile, g > 0);
+        tc::mma_commit(&bars->k_empty[g % 3]);
+      }
+      tc::mma_commit(&bars->drain);
+      tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+    }
+  } else {
+    // ------------------------------------------------------------ elementwise
+    const int q = warp & 3, half = (warp - 2) >> 2;      // TMEM lane quarter; first or second 64 keys of a tile
+    const int r = q * 32 + lane, i = i0 + r / a.G, hq = h * a.G + r % a.G;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const bool valid = r < qpt * a.G && i < a.Sq;
+    DenseRow row{0, 0, 0, 0.f};
+    float lse2 = 0.f, delta = 0.f;
+    if (valid) {
+      row = dense_row(a, seq, b, hq, i);
+      const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + i;
+      lse2 = a.lse[flat] * kLog2e;
+      delta = a.delta[flat];
+    }
+    const float cap2 = a.cap * kLog2e, in = CAP ? a.scale / a.cap * (2.f * kLog2e) : 0.f, scale2 = a.scale * kLog2e;
+    const float slope2 = row.slope * kLog2e;
+    bool ok = true;
+    uint32_t g = 0;
+    for (int j; (j = walk.next(lane)) >= 0; ++g) {
+      const uint32_t colS = tbase + lanes + (g & 1 ? kColB : kColA) + half * 64;
+      const uint32_t colP = tbase + lanes + L::kColDp + half * 64;
+      const int first = j * kT + half * 64;
+      if (!warp_wait(&bars->s_full[g & 1], (g >> 1) & 1, abort)) {
+        fail(&bars->abort, 10);
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      float pw[64];
+      const uint64_t see = visible64(row, doc_k, doc_k != nullptr ? walk.docs[j] : make_int2(0, 0), first);
+      const float far = (float)(row.pos - first);
+#pragma unroll
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        uint32_t s[32];
+        tc::tmem_ld32(colS + c0, s);
+        tc::tmem_ld_wait();
+        const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float x = __uint_as_float(s[c]);
+          float y, dcap = 1.f;
+          if (CAP) {
+            const float th = fmaf(-2.f, rcp(1.f + ex2(x * in)), 1.f);
+            y = fmaf(cap2, th, -lse2);
+            dcap = fmaf(-th, th, 1.f);
+          } else {
+            y = fmaf(x, scale2, -lse2);
+          }
+          if (BIAS) y = fmaf(-slope2, fabsf(far - (float)(c0 + c)), y);
+          const float p = (bits >> c) & 1u ? ex2(y) : 0.f;
+          pw[c0 + c] = CAP ? p * dcap : p;
+        }
+      }
+      if (!warp_wait(&bars->dp_full, g & 1, abort)) {
+        fail(&bars->abort, 11);
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+#pragma unroll
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        uint32_t dp[32], packed[16];
+        tc::tmem_ld32(colP + c0, dp);
+        tc::tmem_ld_wait();
+        const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float d0 = pw[c0 + c] * (__uint_as_float(dp[c]) - delta);
+          float d1 = pw[c0 + c + 1] * (__uint_as_float(dp[c + 1]) - delta);
+          if (!((bits >> c) & 1u)) d0 = 0.f;            // dP of a masked pair may be anything
+          if (!((bits >> (c + 1)) & 1u)) d1 = 0.f;
+          packed[c / 2] = pack_bf16(d0, d1);
+        }
+        tc::tmem_st16(colS + c0 / 2, packed);           // over the scores of this half, which are in registers
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+    }
+    if (n > 0 && ok) {
+      if (!warp_wait(&bars->drain, 0, abort)) fail(&bars->abort, 12);
+      tc::fence_after_sync();
+    }
+    const bool broken = __any_sync(0xffffffffu, *abort != 0);
+    const float by = broken ? __int_as_float(0x7fffffff) : a.scale;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + (int64_t)b * a.dqs.b + (int64_t)hq * a.dqs.h +
+                         (int64_t)i * a.dqs.s;
+    // each half writes its half of the dims
+#pragma unroll 1
+    for (int cc = half * (D / 64); cc < (half + 1) * (D / 64); ++cc) {
+      uint32_t o[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = 0u;
+      if (n > 0 && !broken) {
+        tc::tmem_ld32(tbase + lanes + L::kColQ + cc * 32, o);
+        tc::tmem_ld_wait();
+      }
+      if (valid) store32(dst + cc * 32, o, by);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tbase, 512);
+  if (threadIdx.x == 0 && bars->abort && a.status != nullptr)
+    report_error(a.status, FVATTN_ERR_TIMEOUT, 400 + bars->abort);
+}
+
+// All of TMEM is one CTA's, so no second one may share the SM: it would wait for the first to leave.
+constexpr size_t kAloneBytes = 120 * 1024;
+
+template <int D, bool CAP, bool BIAS>
+cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
+  const int qpt = kTileRows / a.G;
+  CUtensorMap mq, mg, mk, mv;
+  if (!make_map_rows(&mq, a.q, a.qs, a, qpt) || !make_map_rows(&mg, a.dout, a.dos, a, qpt) ||
+      !make_map_keys(&mk, a.k, a.ks, a, kT) || !make_map_keys(&mv, a.v, a.vs, a, kT))
+    return cudaErrorInvalidValue;
+  {
+    auto* kernel = dense_dkv_tc_kernel<D, CAP, BIAS>;
+    const size_t smem = imax<size_t>(DkvLayout<D>::kBytes + 1024, kAloneBytes);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3((unsigned)((a.Sk + kT - 1) / kT), a.Hkv, a.B), kThreads, smem, st>>>(mq, mg, mk, mv, a, qpt);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  auto* kernel = dense_dq_tc_kernel<D, CAP, BIAS>;
+  const size_t smem = imax<size_t>(DqLayout<D>::kBytes + 1024, kAloneBytes);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3((unsigned)((a.Sq + qpt - 1) / qpt), a.Hkv, a.B), kThreads, smem, st>>>(mq, mg, mk, mv, a, qpt);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const DenseArgs& a, cudaStream_t st) {
+  const bool cap = a.cap > 0.f, bias = a.mask.slopes != nullptr;
+  if (cap) return bias ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
+  return bias ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_bwd_tc(const DenseArgs& a, cudaStream_t st) {
+  return a.d == 128 ? launch_d<128>(a, st) : launch_d<64>(a, st);
+}
+
+}  // namespace fv

@@ -296,25 +296,25 @@ __global__ void __launch_bounds__(kThreads) dense_delta_kernel(const DenseArgs a
   if (lane == 0) a.delta[flat] = pad ? 0.f : acc;
 }
 
-// The documents of each 64-token block of doc [B][S], one warp per block: see doc_low().
-__global__ void __launch_bounds__(kThreads) dense_doc_kernel(const int32_t* doc, int2* blocks, int B, int S) {
-  const int nb = (S + kBlock - 1) / kBlock, lane = threadIdx.x & 31;
+// The documents of each block of `block` tokens of doc [B][S], one warp per block: x = the lowest
+// number, with the sign bit set when the block has padding tokens (0x7fffffff without any document),
+// y = the highest (-1 without any).
+__global__ void __launch_bounds__(kThreads) dense_doc_kernel(const int32_t* doc, int2* blocks, int B, int S, int block) {
+  const int nb = (S + block - 1) / block, lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (w >= (int64_t)B * nb) return;
   const int64_t b = w / nb, j = w - b * nb;
   int lo = 0x7fffffff, hi = -1;
   bool pad = false;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int64_t t = j * kBlock + u * 32 + lane;
-    if (t < S) {
-      const int v = doc[b * S + t];
-      if (v < 0) {
-        pad = true;
-      } else {
-        lo = min(lo, v);
-        hi = max(hi, v);
-      }
+  for (int u = lane; u < block; u += 32) {
+    const int64_t t = j * block + u;
+    if (t >= S) break;
+    const int v = doc[b * S + t];
+    if (v < 0) {
+      pad = true;
+    } else {
+      lo = min(lo, v);
+      hi = max(hi, v);
     }
   }
   lo = __reduce_min_sync(0xffffffffu, lo);
@@ -511,18 +511,10 @@ cudaError_t launch_dense_f32(const DenseArgs& a, cudaStream_t st) {
 cudaError_t launch_dense_f32_bwd(const DenseArgs& a, cudaStream_t st) {
   return a.d == 128 ? bwd_d<float, 128>(a, st) : bwd_d<float, 64>(a, st);
 }
-cudaError_t launch_dense_simple_bf16(const DenseArgs& a, cudaStream_t st) {
-  return a.d == 128 ? fwd_d<__nv_bfloat16, 128>(a, st) : fwd_d<__nv_bfloat16, 64>(a, st);
-}
-cudaError_t launch_dense_simple_bf16_bwd(const DenseArgs& a, cudaStream_t st) {
-  return a.d == 128 ? bwd_d<__nv_bfloat16, 128>(a, st) : bwd_d<__nv_bfloat16, 64>(a, st);
-}
-
-cudaError_t launch_dense_docs(const DenseArgs& a, bool queries, cudaStream_t st) {
-  const int S = queries ? a.Sq : a.Sk;
-  const int64_t warps = (int64_t)a.B * ((S + kBlock - 1) / kBlock);
-  dense_doc_kernel<<<(unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(
-      queries ? a.mask.doc_q : a.mask.doc_k, queries ? a.doc_blocks_q : a.doc_blocks_k, a.B, S);
+cudaError_t launch_dense_docs(const int32_t* doc, int2* blocks, int B, int S, int block, cudaStream_t st) {
+  const int64_t warps = (int64_t)B * ((S + block - 1) / block);
+  dense_doc_kernel<<<(unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(doc, blocks, B, S,
+                                                                                                 block);
   return cudaGetLastError();
 }
 

@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     __syncthreads();
   }
   const uint32_t tbase = bars->tmem_base;
-  BlockWalk walk(a, b, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
+  const int2* docs = a.doc_blocks_k != nullptr ? a.doc_blocks_k + (int64_t)b * ((a.Sk + kBlock - 1) / kBlock) : nullptr;
+  BlockWalk walk(docs, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
 
   if (warp == 0) {
     // ------------------------------------------------------------ Q and K loader
@@ -171,9 +172,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         break;
       }
       unsigned char* dst = sV + st * L::kKBytes;
-      if (dirty_block(a, seq, b, j)) {
-        // keys that do not exist: zeros, whatever their memory holds (0 * NaN would reach O)
-        copy_keys<D>(dst, static_cast<const __nv_bfloat16*>(a.v) + b * a.vs.b + h * a.vs.h, a.vs.s, j * kBlock, kBlock,
+      // keys that do not exist although their memory does: zeros, whatever it holds (0 * NaN would reach O)
+      if ((seq.kv < a.Sk && (j + 1) * kBlock > seq.kv) || (docs != nullptr && docs[j].x < 0)) {
+        copy_keys<D>(dst, static_cast<const __nv_bfloat16*>(a.v) + (int64_t)b * a.vs.b + (int64_t)h * a.vs.h, a.vs.s, j * kBlock, kBlock,
                      seq.kv, a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr, lane, 32);
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           tc::tmem_ld_wait();
         }
         map.template apply<64>(sraw, row.pos - j * kBlock);
-        const uint64_t see = visible64(a, row, doc_k, walk, j);
+        const uint64_t see = visible64(row, doc_k, docs != nullptr ? docs[j] : make_int2(0, 0), j * kBlock);
         if (__any_sync(0xffffffffu, see != ~0ull)) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {

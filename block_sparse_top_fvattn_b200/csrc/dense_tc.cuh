@@ -93,24 +93,22 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* out, __nv_bfloat16* r
   }
 }
 
-// The documents of the 64-token blocks of a sequence (dense_doc_kernel): x = the lowest number, with the
+// The documents of a sequence's blocks of tokens (dense_doc_kernel): x = the lowest number, with the
 // sign bit set when the block has padding tokens too (0x7fffffff without any document); y = the
 // highest (-1 without any).
 __device__ __forceinline__ int doc_low(int2 v) { return v.x & 0x7fffffff; }
 __device__ __forceinline__ bool doc_uniform(int2 v) { return v.x == v.y; }      // one document, no padding
 
-// Ascending walk over the 64-key blocks [j, end) that a set of documents [lo, hi] can see. Used by
-// whole warps: with documents a warp tests 32 blocks at a time.
+// Ascending walk over the blocks [j, end) of tokens whose documents meet the range [lo, hi] (every block
+// without documents). Used by whole warps: with documents a warp tests 32 blocks at a time.
 struct BlockWalk {
   const int2* docs;       // null without documents
   int j, end, lo, hi;
   uint32_t word;          // blocks of the current window that are left
-  int base;               // its first block; -1 before the first window
+  int base;               // its first block
 
-  __device__ __forceinline__ BlockWalk(const DenseArgs& a, int b, int begin, int stop, int lo_, int hi_)
-      : docs(nullptr), j(begin), end(stop), lo(lo_), hi(hi_), word(0), base(begin) {
-    if (a.mask.doc_k != nullptr) docs = a.doc_blocks_k + (int64_t)b * ((a.Sk + kBlock - 1) / kBlock);
-  }
+  __device__ __forceinline__ BlockWalk(const int2* docs_, int begin, int stop, int lo_, int hi_)
+      : docs(docs_), j(begin), end(stop), lo(lo_), hi(hi_), word(0), base(begin) {}
   __device__ __forceinline__ uint32_t window(int at, int lane) const {
     bool see = false;
     if (at + lane < end) {
@@ -139,26 +137,18 @@ struct BlockWalk {
   }
 };
 
-// Whether block j has keys that do not exist although their memory does.
-__device__ __forceinline__ bool dirty_block(const DenseArgs& a, const DenseSeq& s, int b, int j) {
-  if (s.kv < a.Sk && (j + 1) * kBlock > s.kv) return true;
-  return a.mask.doc_k != nullptr && a.doc_blocks_k[(int64_t)b * ((a.Sk + kBlock - 1) / kBlock) + j].x < 0;
-}
-
-// Bit c: key 64 j + c is visible to the row.
-__device__ __forceinline__ uint64_t visible64(const DenseArgs& a, const DenseRow& row, const int32_t* doc_k,
-                                              const BlockWalk& walk, int j) {
-  const int n = row.limit - j * kBlock;
-  uint64_t see = n >= kBlock ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+// Bit c: key first + c is visible to the row; v: the documents of the block it lies in.
+__device__ __forceinline__ uint64_t visible64(const DenseRow& row, const int32_t* doc_k, int2 v, int first) {
+  const int n = row.limit - first;
+  uint64_t see = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
   if (doc_k != nullptr) {
-    const int2 v = walk.docs[j];
     if (doc_uniform(v)) {
       if (v.y != row.doc) see = 0ull;
     } else if (see != 0ull) {
       // bits of keys at or past Sk are clear already: their document numbers are not read
       uint64_t same = 0ull;
-      for (int c = 0; c < kBlock; ++c)
-        if ((see >> c) & 1ull) same |= (uint64_t)(doc_k[j * kBlock + c] == row.doc) << c;
+      for (int c = 0; c < 64; ++c)
+        if ((see >> c) & 1ull) same |= (uint64_t)(doc_k[first + c] == row.doc) << c;
       see &= same;
     }
   }
@@ -206,6 +196,22 @@ __device__ __forceinline__ void copy_keys(unsigned char* dst, const __nv_bfloat1
     if (t0 + r < end && (doc == nullptr || doc[t0 + r] >= 0))
       v = *reinterpret_cast<const uint4*>(base + (int64_t)(t0 + r) * stride + c * 8);
     *reinterpret_cast<uint4*>(dst + (c / 8) * rows * 128 + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v;
+  }
+}
+
+// The rows of `queries` queries from i0 of a key head's group into a tile of 128 rows, in the order of
+// make_map_rows; zeros for queries at or past Sq and for padding ones.
+template <int D>
+__device__ __forceinline__ void copy_rows(unsigned char* dst, const __nv_bfloat16* base, const fvattn_strides& s,
+                                          const DenseArgs& a, int b, int h, int i0, int queries, const int32_t* doc,
+                                          int me, int of) {
+  for (int x = me; x < queries * a.G * (D / 8); x += of) {
+    const int r = x / (D / 8), c = x % (D / 8), i = i0 + r / a.G;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (i < a.Sq && (doc == nullptr || doc[i] >= 0))
+      v = *reinterpret_cast<const uint4*>(base + (int64_t)b * s.b + (int64_t)(h * a.G + r % a.G) * s.h + (int64_t)i * s.s +
+                                          c * 8);
+    *reinterpret_cast<uint4*>(dst + (c / 8) * kTileRows * 128 + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v;
   }
 }
 
