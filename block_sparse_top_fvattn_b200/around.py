@@ -9,6 +9,7 @@ positive multiples of 16 bytes (slices of a fused projection, places in a cache,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 from typing import Optional, Tuple
@@ -29,8 +30,9 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     raise TypeError(f"{name}: unsupported dtype {t.dtype}; bf16 or fp32")
 
 
-def _check(t: torch.Tensor, name: str, shape, like: torch.Tensor, dtype=None) -> torch.Tensor:
-    """A 4-D operand: on like's device, of its dtype, the last dimension contiguous."""
+def _check(t: torch.Tensor, name: str, shape, like: torch.Tensor, dtype=None) -> None:
+    """An operand: on like's device, of its dtype (or the given one); a 4-D one with a contiguous last
+    dimension, others contiguous. The library checks base addresses."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != like.device:
@@ -41,13 +43,11 @@ def _check(t: torch.Tensor, name: str, shape, like: torch.Tensor, dtype=None) ->
         raise ValueError(f"{name} must have dtype {dtype or like.dtype}, not {t.dtype}")
     if t.dim() == 4:
         unit = 16 // t.element_size()
-        if t.stride(3) != 1 or t.data_ptr() % 16 or any(
-                n > 1 and (s <= 0 or s % unit) for n, s in zip(t.shape[:3], t.stride()[:3])):
-            raise ValueError(f"{name}: the last dimension must be contiguous, the base and the other strides "
-                             f"multiples of 16 bytes, and no dimension expanded (strides {tuple(t.stride())})")
+        if t.stride(3) != 1 or any(n > 1 and (s <= 0 or s % unit) for n, s in zip(t.shape[:3], t.stride()[:3])):
+            raise ValueError(f"{name}: the last dimension must be contiguous, the other strides multiples of 16 "
+                             f"bytes, and no dimension expanded (strides {tuple(t.stride())})")
     elif not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
 
 
 def _strides(t: torch.Tensor, tokens_first: bool = False) -> _lib.Strides:
@@ -56,47 +56,69 @@ def _strides(t: torch.Tensor, tokens_first: bool = False) -> _lib.Strides:
     return _lib.Strides(b, y, x) if tokens_first else _lib.Strides(b, x, y)
 
 
-class _On:
-    """The device and stream of a call; scratch and outputs made in it are kept from reuse by other
-    streams until the call's stream has passed them."""
-
-    def __init__(self, like: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-        self.device = like.device
-        self.guard = torch.cuda.device(self.device)
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
-        self.stream = stream
-
-    def __enter__(self):
-        self.guard.__enter__()
-        self.current = torch.cuda.current_stream(self.device)
-        self.handle = ctypes.c_void_p((self.stream or self.current).cuda_stream)
-        return self
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
-
-    def made(self, t: torch.Tensor) -> torch.Tensor:
-        if self.stream is not None and self.stream != self.current and t.numel():
-            t.record_stream(self.stream)
-        return t
-
-    def scratch(self, nbytes: int, given: Optional[torch.Tensor] = None) -> torch.Tensor:
-        if given is not None:
-            if not given.is_cuda or given.device != self.device or not given.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor on the device of the call")
-            if given.numel() * given.element_size() < nbytes:
-                raise ValueError(f"workspace needs {nbytes} bytes")
-            return given
-        return self.made(torch.empty(nbytes, dtype=torch.uint8, device=self.device))
-
-
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _status(t: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
-    return None if t is None else _check(t, "status", (4,), like, torch.int32)
+# Checking the tensors of a call and describing them to the library takes longer than a small call
+# runs, so both are done once per description (shapes, strides, types, devices and options, never
+# addresses or contents) and kept here; calls over ever new lengths start it afresh now and then.
+_PLANS_MOST = 512
+_plans: dict = {}
+
+
+def _meta(t: Optional[torch.Tensor]):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _keep(key, plan):
+    if len(_plans) >= _PLANS_MOST:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+class _Plan:
+    """A checked description of a call: the library's structures, the output shapes, scratch bytes."""
+
+    def __init__(self, shape, device, nws=0, out_shapes=()):
+        self.shape, self.ref, self.device = shape, ctypes.byref(shape), device
+        self.nws, self.out_shapes = nws, out_shapes
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _current(device: torch.device):
+    """Makes the device of a call current around its launches."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _handle(device: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream
+
+
+def _made(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A tensor made in a call that runs on `stream`: its memory is not reused before that has passed."""
+    if stream is not None and t.numel():
+        t.record_stream(stream)
+    return t
+
+
+def _scratch(plan: _Plan, given: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
+    if given is not None:
+        if given.device != plan.device or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the device of the call")
+        if given.numel() * given.element_size() < plan.nws:
+            raise ValueError(f"workspace needs {plan.nws} bytes")
+        return given
+    if plan.nws == 0:
+        return None
+    return _made(torch.empty(plan.nws, dtype=torch.uint8, device=plan.device), stream)
 
 
 # ------------------------------------------------------------------ norm and rotation
@@ -141,6 +163,38 @@ def _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps) -
     return _lib.QkShape(B, S, Hq, k.shape[2], d, dt, wdt, rot, int(bool(interleaved)), float(eps), rows)
 
 
+def _qk_plan(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps, outs, grads, status) -> _Plan:
+    """outs: q_out, k_out or their gradients; grads: dq, dk of the gradients' call, None in the other."""
+    key = ("qk", _meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos), _meta(sin), _meta(positions),
+           _meta(outs[0]), _meta(outs[1]), bool(interleaved), float(eps), _meta(status),
+           None if grads is None else (_meta(grads[0]), _meta(grads[1])))
+    plan = _plans.get(key)
+    if plan is not None:
+        return plan
+    shp = _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps)
+    if status is not None:
+        _check(status, "status", (4,), q, torch.int32)
+    shapes = ((shp.B, shp.Hq, shp.S, shp.d), (shp.B, shp.Hk, shp.S, shp.d))
+
+    def strides(given, names, want, tokens_first):
+        for t, name, n in zip(given, names, want):
+            if t is None:                      # made by the call: dense
+                yield _lib.Strides(n[1] * n[2] * n[3], *((n[3], n[2] * n[3]) if tokens_first else (n[2] * n[3], n[3])))
+            else:
+                _check(t, name, n, q)
+                yield _strides(t, tokens_first)
+
+    shp.q, shp.k = _strides(q, True), _strides(k, True)
+    names = ("q_out", "k_out") if grads is None else ("dq_out", "dk_out")
+    shp.qo, shp.ko = strides(outs, names, shapes, False)
+    nws = 0
+    if grads is not None:
+        shp.dq, shp.dk = strides(grads, ("dq", "dk"), (q.shape, k.shape), True)
+        if q_weight is not None:
+            nws = int(load().fvattn_qk_norm_rope_workspace_bytes(ctypes.byref(shp)))
+    return _keep(key, _Plan(shp, q.device, nws, shapes))
+
+
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
                  k_weight: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
                  sin: Optional[torch.Tensor] = None, *, positions: Optional[torch.Tensor] = None,
@@ -156,19 +210,16 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     outside the tables gives NaN rows, and FVATTN_ERR_INVALID in `status` (int32 [4], zeroed by the
     caller) when given. interleaved: pairs (2i, 2i + 1), else (i, i + rot / 2). q_out, k_out: where to
     write, e.g. a place in a cache."""
-    shp = _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps)
-    with _On(q, stream) as on:
-        _status(status, q)
-        if q_out is None:
-            q_out = on.made(torch.empty((shp.B, shp.Hq, shp.S, shp.d), dtype=q.dtype, device=q.device))
-        if k_out is None:
-            k_out = on.made(torch.empty((shp.B, shp.Hk, shp.S, shp.d), dtype=q.dtype, device=q.device))
-        _check(q_out, "q_out", (shp.B, shp.Hq, shp.S, shp.d), q)
-        _check(k_out, "k_out", (shp.B, shp.Hk, shp.S, shp.d), q)
-        shp.q, shp.k, shp.qo, shp.ko = _strides(q, True), _strides(k, True), _strides(q_out), _strides(k_out)
-        check(load().fvattn_qk_norm_rope(q.data_ptr(), k.data_ptr(), ctypes.byref(shp), _ptr(q_weight),
-                                         _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), q_out.data_ptr(),
-                                         k_out.data_ptr(), _ptr(status), on.handle), "fvattn_qk_norm_rope")
+    plan = _qk_plan(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps, (q_out, k_out), None, status)
+    handle = _handle(plan.device, stream)
+    if q_out is None:
+        q_out = _made(torch.empty(plan.out_shapes[0], dtype=q.dtype, device=plan.device), stream)
+    if k_out is None:
+        k_out = _made(torch.empty(plan.out_shapes[1], dtype=q.dtype, device=plan.device), stream)
+    with _current(plan.device):
+        check(load().fvattn_qk_norm_rope(q.data_ptr(), k.data_ptr(), plan.ref, _ptr(q_weight), _ptr(k_weight), _ptr(cos),
+                                         _ptr(sin), _ptr(positions), q_out.data_ptr(), k_out.data_ptr(), _ptr(status),
+                                         handle), "fvattn_qk_norm_rope")
     return q_out, k_out
 
 
@@ -182,31 +233,22 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     """fvattn_qk_norm_rope_bwd: gradients of qk_norm_rope for the output gradients dq_out
     [B, Hq, S, d] and dk_out [B, Hk, S, d]. Returns (dq, dk, dq_weight, dk_weight): dq, dk like q, k;
     the weights' gradients in fp32, None without weights. Equal calls give equal bits."""
-    shp = _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps)
-    _check(dq_out, "dq_out", (shp.B, shp.Hq, shp.S, shp.d), q)
-    _check(dk_out, "dk_out", (shp.B, shp.Hk, shp.S, shp.d), q)
-    with _On(q, stream) as on:
-        _status(status, q)
-        if dq is None:
-            dq = on.made(torch.empty(q.shape, dtype=q.dtype, device=q.device))
-        if dk is None:
-            dk = on.made(torch.empty(k.shape, dtype=k.dtype, device=q.device))
-        _check(dq, "dq", q.shape, q)
-        _check(dk, "dk", k.shape, q)
-        shp.q, shp.k, shp.dq, shp.dk = _strides(q, True), _strides(k, True), _strides(dq, True), _strides(dk, True)
-        shp.qo, shp.ko = _strides(dq_out), _strides(dk_out)
-        dwq = dwk = None
-        if q_weight is not None:
-            dwq = on.made(torch.empty(shp.d, dtype=torch.float32, device=q.device))
-            dwk = on.made(torch.empty(shp.d, dtype=torch.float32, device=q.device))
-        lib = load()
-        nws = int(lib.fvattn_qk_norm_rope_workspace_bytes(ctypes.byref(shp))) if dwq is not None else 0
-        ws = on.scratch(nws, workspace)
-        check(lib.fvattn_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-                                          ctypes.byref(shp), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-                                          _ptr(positions), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk),
-                                          ws.data_ptr() if nws else None, nws, _ptr(status), on.handle),
-              "fvattn_qk_norm_rope_bwd")
+    plan = _qk_plan(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps, (dq_out, dk_out), (dq, dk), status)
+    handle = _handle(plan.device, stream)
+    if dq is None:
+        dq = _made(torch.empty(q.shape, dtype=q.dtype, device=plan.device), stream)
+    if dk is None:
+        dk = _made(torch.empty(k.shape, dtype=q.dtype, device=plan.device), stream)
+    dwq = dwk = None
+    if q_weight is not None:
+        dwq = _made(torch.empty(q.shape[3], dtype=torch.float32, device=plan.device), stream)
+        dwk = _made(torch.empty(q.shape[3], dtype=torch.float32, device=plan.device), stream)
+    ws = _scratch(plan, workspace, stream)
+    with _current(plan.device):
+        check(load().fvattn_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), plan.ref,
+                                             _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
+                                             dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), plan.nws,
+                                             _ptr(status), handle), "fvattn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -234,7 +276,8 @@ class AttnConfig:
     doc_q: Optional[torch.Tensor] = None
     doc_k: Optional[torch.Tensor] = None
 
-    def to_c(self, q: torch.Tensor, Sk: int) -> _lib.DenseMask:
+    def check(self, q: torch.Tensor, Sk: int) -> None:
+        """Raises ValueError unless the configuration fits queries q and Sk keys."""
         B, Hq, Sq, _ = q.shape
         if not 0 <= self.softcap < float("inf"):
             raise ValueError("softcap must be finite and >= 0")
@@ -248,6 +291,8 @@ class AttnConfig:
             t = getattr(self, name)
             if t is not None:
                 _check(t, name, shape, q, dtype)
+
+    def to_c(self) -> _lib.DenseMask:
         return _lib.DenseMask(_ptr(self.slopes), _ptr(self.q_start), _ptr(self.kv_len), _ptr(self.prefix_len),
                               _ptr(self.doc_q), _ptr(self.doc_k))
 
@@ -268,6 +313,46 @@ def _dense_shape(q, k, v, cfg: AttnConfig, scale: float) -> _lib.DenseShape:
     return shp
 
 
+def _dense_plan(q, k, v, cfg: AttnConfig, scale, out, rest, lse, status, grads) -> _Plan:
+    """grads: (dout, dq, dk, dv) of the gradients' call, None in the other."""
+    key = ("dense", _meta(q), _meta(k), _meta(v), _meta(out), _meta(rest), _meta(lse), _meta(status), float(scale),
+           float(cfg.softcap), bool(cfg.causal), _meta(cfg.slopes), _meta(cfg.q_start), _meta(cfg.prefix_len), _meta(cfg.kv_len),
+           _meta(cfg.doc_q), _meta(cfg.doc_k), None if grads is None else tuple(map(_meta, grads)))
+    plan = _plans.get(key)
+    if plan is not None:
+        return plan
+    shp = _dense_shape(q, k, v, cfg, scale)
+    cfg.check(q, k.shape[2])
+    if status is not None:
+        _check(status, "status", (4,), q, torch.int32)
+    if lse is not None:
+        _check(lse, "lse", q.shape[:3], q, torch.float32)
+
+    def strides(t, name, like):
+        if t is None:                          # made by the call: dense
+            _, H, S, d = like.shape
+            return _lib.Strides(H * S * d, S * d, d)
+        _check(t, name, like.shape, q)
+        return _strides(t)
+
+    shp.o = strides(out, "out", q)
+    if rest is not None:
+        r = strides(rest, "rest", q)
+        if q.dtype != torch.bfloat16 or (r.b, r.h, r.s) != (shp.o.b, shp.o.h, shp.o.s):
+            raise ValueError("rest must be bf16 and have out's strides")
+    lib = load()
+    mask = ctypes.byref(cfg.to_c())
+    if grads is None:
+        nws = int(lib.fvattn_dense_attn_workspace_bytes(ctypes.byref(shp), mask))
+    else:
+        for name, t, like in zip(("dout", "dq", "dk", "dv"), grads, (q, q, k, v)):
+            setattr(shp, name, strides(t, name, like))
+        nws = int(lib.fvattn_dense_attn_bwd_workspace_bytes(ctypes.byref(shp), mask))
+    if nws == _lib.SIZE_ERROR:
+        return _Plan(shp, q.device)            # the call that follows says what is wrong
+    return _keep(key, _Plan(shp, q.device, nws))
+
+
 def dense_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cfg: Optional[AttnConfig] = None, *,
                out: Optional[torch.Tensor] = None, rest: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -281,27 +366,14 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cfg: Optional[
     optional int32 [4] zeroed by the caller; a wait that ran out in a kernel is reported there and makes
     its rows NaN."""
     cfg = cfg or AttnConfig()
-    shp = _dense_shape(q, k, v, cfg, scale)
-    mask = cfg.to_c(q, k.shape[2])
-    with _On(q, stream) as on:
-        _status(status, q)
-        if out is None:
-            out = on.made(torch.empty(q.shape, dtype=q.dtype, device=q.device))
-        _check(out, "out", q.shape, q)
-        if rest is not None:
-            _check(rest, "rest", q.shape, q)
-            if q.dtype != torch.bfloat16 or rest.stride() != out.stride():
-                raise ValueError("rest must be bf16 and have out's strides")
-        if lse is not None:
-            _check(lse, "lse", q.shape[:3], q, torch.float32)
-        shp.o = _strides(out)
-        lib = load()
-        nws = int(lib.fvattn_dense_attn_workspace_bytes(ctypes.byref(shp), ctypes.byref(mask)))
-        if nws == _lib.SIZE_ERROR:
-            nws = 0                       # the call below says which argument is wrong
-        ws = on.scratch(nws, workspace) if nws or workspace is not None else None
-        check(lib.fvattn_dense_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(shp), ctypes.byref(mask),
-                                    out.data_ptr(), _ptr(rest), _ptr(lse), _ptr(ws), nws, _ptr(status), on.handle),
+    plan = _dense_plan(q, k, v, cfg, scale, out, rest, lse, status, None)
+    handle = _handle(plan.device, stream)
+    if out is None:
+        out = _made(torch.empty(q.shape, dtype=q.dtype, device=plan.device), stream)
+    ws = _scratch(plan, workspace, stream)
+    with _current(plan.device):
+        check(load().fvattn_dense_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()),
+                                       out.data_ptr(), _ptr(rest), _ptr(lse), _ptr(ws), plan.nws, _ptr(status), handle),
               "fvattn_dense_attn")
     return out
 
@@ -316,30 +388,14 @@ def dense_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     its inputs, out, lse and (optionally) rest, with the same cfg and scale. Shared key heads get the
     sum over their query heads. Equal calls give equal bits."""
     cfg = cfg or AttnConfig()
-    shp = _dense_shape(q, k, v, cfg, scale)
-    mask = cfg.to_c(q, k.shape[2])
-    _check(dout, "dout", q.shape, q)
-    _check(out, "out", q.shape, q)
-    _check(lse, "lse", q.shape[:3], q, torch.float32)
-    if rest is not None:
-        _check(rest, "rest", q.shape, q)
-        if q.dtype != torch.bfloat16 or rest.stride() != out.stride():
-            raise ValueError("rest must be bf16 and have out's strides")
-    with _On(q, stream) as on:
-        _status(status, q)
-        dq, dk, dv = (on.made(torch.empty(t.shape, dtype=t.dtype, device=t.device)) if g is None else g
-                      for g, t in ((dq, q), (dk, k), (dv, v)))
-        for g, n, t in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-            _check(g, n, t.shape, q)
-        shp.o, shp.dout = _strides(out), _strides(dout)
-        shp.dq, shp.dk, shp.dv = _strides(dq), _strides(dk), _strides(dv)
-        lib = load()
-        nws = int(lib.fvattn_dense_attn_bwd_workspace_bytes(ctypes.byref(shp), ctypes.byref(mask)))
-        if nws == _lib.SIZE_ERROR:
-            nws = 0
-        ws = on.scratch(max(nws, 16), workspace)
-        check(lib.fvattn_dense_attn_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                        _ptr(rest), lse.data_ptr(), ctypes.byref(shp), ctypes.byref(mask),
-                                        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), nws, _ptr(status),
-                                        on.handle), "fvattn_dense_attn_bwd")
+    plan = _dense_plan(q, k, v, cfg, scale, out, rest, lse, status, (dout, dq, dk, dv))
+    handle = _handle(plan.device, stream)
+    dq, dk, dv = (_made(torch.empty(t.shape, dtype=q.dtype, device=plan.device), stream) if g is None else g
+                  for g, t in ((dq, q), (dk, k), (dv, v)))
+    ws = _scratch(plan, workspace, stream)
+    with _current(plan.device):
+        check(load().fvattn_dense_attn_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                           _ptr(rest), lse.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()), dq.data_ptr(),
+                                           dk.data_ptr(), dv.data_ptr(), _ptr(ws), plan.nws, _ptr(status), handle),
+              "fvattn_dense_attn_bwd")
     return dq, dk, dv

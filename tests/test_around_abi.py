@@ -137,4 +137,4 @@ def test_binding_refuses_cpu_tensors_and_configs():
     for bad in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(prefix_len=torch.zeros(1, dtype=torch.int32)),
                 dict(doc_q=torch.zeros((1, 4), dtype=torch.int32))):
         with pytest.raises(ValueError):
-            fv.AttnConfig(**bad).to_c(q, 4)
+            fv.AttnConfig(**bad).check(q, 4)
