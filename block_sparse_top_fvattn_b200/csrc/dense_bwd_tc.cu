@@ -24,6 +24,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "dense.cuh"
 #include "dense_tc.cuh"
 #include "tc_ptx.cuh"
@@ -82,8 +84,8 @@ __device__ __forceinline__ void store32(__nv_bfloat16* p, uint32_t (&o)[32], flo
 
 // What a row tile's rows need, per stage.
 struct RowStats {
-  float lse2[kT];      // lse log2 e
-  float delta[kT];
+  float nlse2[kT];     // - lse log2 e
+  float ndelta[kT];    // - delta
   float far[kT];       // position minus the first key of the key tile
   float slope2[kT];    // slope log2 e
   int limit[kT];       // visible keys are below it, counted from the first key of the key tile
@@ -106,7 +108,8 @@ struct DkvBars {
   uint64_t g_full[2], g_empty[2];     // dout of a tile
   uint64_t s_full, p_full, dp_full, ds_full;
   uint64_t drain;
-  int masked[2];                      // whether some pair of the tile is not visible
+  int rows[2];                        // rows of the tile that are queries; the others come last
+  int masks[2];                       // whether limits (1) or documents (2) hide pairs of those rows
   int doc_lo, doc_hi, doc_pad;        // documents of the keys
   uint32_t tmem_base;
   int abort;
@@ -116,7 +119,8 @@ template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const DenseArgs a, const int qpt) {
+                        const DenseArgs a, const int qpt,
+                       const TileOrder order) {
   using L = DkvLayout<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -125,7 +129,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   RowStats* stats = reinterpret_cast<RowStats*>(smem + L::kOffStats);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
-  const int h = blockIdx.y, b = blockIdx.z, j0 = blockIdx.x * kT;
+  int x, bh;
+  tile_of(order, blockIdx.x, x, bh);        // the first keys are seen by the most rows under an order
+  const int b = bh / a.Hkv, h = bh - b * a.Hkv, j0 = x * kT;
   const DenseSeq seq = dense_seq(a, b);
   const int32_t* doc_q = a.mask.doc_q != nullptr ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
   const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
@@ -228,31 +234,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       q_par[s] = (int)par;
       // row statistics
       RowStats& st = stats[s];
-      bool full = true;
+      const int rows = min(qpt, a.Sq - i0) * a.G;
+      bool limits = false, docs = false;
 #pragma unroll
       for (int u = 0; u < kT / 32; ++u) {
-        const int r = u * 32 + lane, i = i0 + r / a.G;
+        const int r = u * 32 + lane;
         DenseRow row{0, -1, 0, 0.f};
         float lse = 0.f, delta = 0.f;
-        if (r < qpt * a.G && i < a.Sq) {
-          const int hq = h * a.G + r % a.G;
+        if (r < rows) {
+          const int i = i0 + r / a.G, hq = h * a.G + r % a.G;
           row = dense_row(a, seq, b, hq, i);
           const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + i;
           lse = a.lse[flat];
           delta = a.delta[flat];
+          limits = limits || row.limit - j0 < jend;
+          docs = docs || (doc_q != nullptr && row.doc != bars->doc_lo);
         }
-        st.lse2[r] = lse * kLog2e;
-        st.delta[r] = delta;
+        st.nlse2[r] = -lse * kLog2e;
+        st.ndelta[r] = -delta;
         st.far[r] = (float)(row.pos - j0);
         st.slope2[r] = row.slope * kLog2e;
         st.limit[r] = row.limit - j0;
         st.doc[r] = row.doc;
-        full = full && row.limit - j0 >= jend && (doc_q == nullptr || (row.doc == bars->doc_lo));
       }
-      full = __all_sync(0xffffffffu, full);
+      limits = __any_sync(0xffffffffu, limits);
+      docs = __any_sync(0xffffffffu, docs) || (doc_k != nullptr && (bars->doc_lo != bars->doc_hi || bars->doc_pad));
       if (lane == 0) {
-        // keys that do not exist need no mask here: they reach only their own results, written as zeros
-        bars->masked[s] = !(full && (doc_k == nullptr || (bars->doc_lo == bars->doc_hi && !bars->doc_pad)));
+        bars->rows[s] = rows;
+        bars->masks[s] = (limits ? 1 : 0) | (docs ? 2 : 0);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->q_full[s]);
@@ -331,10 +340,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t colS = tbase + lanes + kColA + half * 64, colP = tbase + lanes + kColB + half * 64;
     const int my_doc = doc_k != nullptr && j < a.Sk ? doc_k[j] : 0;
     const bool key_ok = j < seq.kv && my_doc >= 0;
-    const float cap2 = a.cap * kLog2e, in = CAP ? a.scale / a.cap * (2.f * kLog2e) : 0.f, scale2 = a.scale * kLog2e;
-    const float fr = (float)r;
+    const float in = CAP ? a.scale / a.cap : 0.f, factor = (CAP ? a.cap : a.scale) * kLog2e, fr = (float)r;
+    const uint64_t factor2 = f2(factor, factor);
+    uint64_t pw[32];       // P, then P times the cap's derivative, in pairs
+    uint64_t see = ~0ull;  // bit c: row c of this half sees this lane's key
+    uint32_t g = 0;
+
+    // P^T of this half's rows over the scores it is made from (columns 0-31 of the half, loaded by then)
+    auto probs = [&](auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+      const RowStats& st = stats[g & 1];
+#pragma unroll
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        uint32_t s[32], packed[16];
+        tc::tmem_ld32(colS + c0, s);
+        tc::tmem_ld_wait();
+        if (CAP) tanh32(s, in);
+        const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const int at = half * 64 + c0 + c;
+          const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(&st.nlse2[at]);
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const uint64_t t2 = f2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1]));
+            float y0, y1;
+            f2_split(ffma2(t2, factor2, e == 0 ? l4.x : l4.y), y0, y1);
+            if (BIAS) {
+              y0 = fmaf(-st.slope2[at + e], fabsf(st.far[at + e] - fr), y0);
+              y1 = fmaf(-st.slope2[at + e + 1], fabsf(st.far[at + e + 1] - fr), y1);
+            }
+            float p0 = ex2(y0), p1 = ex2(y1);
+            if (MASK) {
+              p0 = (bits >> (c + e)) & 1u ? p0 : 0.f;
+              p1 = (bits >> (c + e + 1)) & 1u ? p1 : 0.f;
+            }
+            packed[(c + e) / 2] = pack_bf16(p0, p1);
+            pw[(c0 + c + e) / 2] = CAP ? times_dcap(f2(p0, p1), t2) : f2(p0, p1);
+          }
+        }
+        tc::tmem_st16(colS + c0 / 2, packed);
+      }
+    };
+    // dS^T over dP^T
+    auto grads = [&](auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+      const RowStats& st = stats[g & 1];
+#pragma unroll
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        uint32_t dp[32], packed[16];
+        tc::tmem_ld32(colP + c0, dp);
+        tc::tmem_ld_wait();
+        const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const ulonglong2 d4 = *reinterpret_cast<const ulonglong2*>(&st.ndelta[half * 64 + c0 + c]);
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            float d0, d1;
+            f2_split(fmul2(pw[(c0 + c + e) / 2], fadd2(f2(__uint_as_float(dp[c + e]), __uint_as_float(dp[c + e + 1])),
+                                                       e == 0 ? d4.x : d4.y)), d0, d1);
+            if (MASK) {                       // dP of a hidden pair may be anything
+              d0 = (bits >> (c + e)) & 1u ? d0 : 0.f;
+              d1 = (bits >> (c + e + 1)) & 1u ? d1 : 0.f;
+            }
+            packed[(c + e) / 2] = pack_bf16(d0, d1);
+          }
+        }
+        tc::tmem_st16(colP + c0 / 2, packed);
+      }
+    };
+
     bool ok = true;
-    for (uint32_t g = 0; g < n; ++g) {
+    for (; g < n; ++g) {
       const RowStats& st = stats[g & 1];
       if (!warp_wait(&bars->q_full[g & 1], (g >> 1) & 1, abort) || !warp_wait(&bars->s_full, g & 1, abort)) {
         fail(&bars->abort, 10);
@@ -342,60 +420,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc::fence_after_sync();
-      // pw: P, then P times the cap's derivative
-      float pw[64];
-      uint64_t see = ~0ull;
-      if (bars->masked[g & 1]) {
-        see = 0ull;
-        if (key_ok) {
-#pragma unroll 8
-          for (int c = 0; c < 64; ++c) {
-            const int cc = half * 64 + c;
-            const bool v = r < st.limit[cc] && (doc_k == nullptr || st.doc[cc] == my_doc);
-            see |= (uint64_t)v << c;
-          }
+      see = low64(bars->rows[g & 1] - half * 64);
+      const int masks = bars->masks[g & 1];
+      if (masks & 1) {
+        uint64_t below = 0ull;
+#pragma unroll 4
+        for (int c = 0; c < 64; c += 4) {
+          const int4 l = *reinterpret_cast<const int4*>(&st.limit[half * 64 + c]);
+          below |= (uint64_t)((r < l.x) | (r < l.y) << 1 | (r < l.z) << 2 | (r < l.w) << 3) << c;
         }
+        see &= below;
       }
-#pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t s[32], packed[16];
-        tc::tmem_ld32(colS + c0, s);
-        tc::tmem_ld_wait();
-        const uint32_t bits = (uint32_t)(see >> c0);
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const int at = half * 64 + c0 + c;
-          const float4 l4 = *reinterpret_cast<const float4*>(&st.lse2[at]);
-          const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-          float f[4], sl[4];
-          if (BIAS) {
-            const float4 f4 = *reinterpret_cast<const float4*>(&st.far[at]);
-            const float4 s4 = *reinterpret_cast<const float4*>(&st.slope2[at]);
-            f[0] = f4.x; f[1] = f4.y; f[2] = f4.z; f[3] = f4.w;
-            sl[0] = s4.x; sl[1] = s4.y; sl[2] = s4.z; sl[3] = s4.w;
-          }
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = __uint_as_float(s[c + e]);
-            float y, dcap = 1.f;
-            if (CAP) {
-              const float t = fmaf(-2.f, rcp(1.f + ex2(x * in)), 1.f);
-              y = fmaf(cap2, t, -l[e]);
-              dcap = fmaf(-t, t, 1.f);
-            } else {
-              y = fmaf(x, scale2, -l[e]);
-            }
-            if (BIAS) y = fmaf(-sl[e], fabsf(f[e] - fr), y);
-            p[e] = (bits >> (c + e)) & 1u ? ex2(y) : 0.f;
-            pw[c0 + c + e] = CAP ? p[e] * dcap : p[e];
-          }
-          packed[c / 2] = pack_bf16(p[0], p[1]);
-          packed[c / 2 + 1] = pack_bf16(p[2], p[3]);
-        }
-        // P^T over the scores it was made from: columns 0-31 of this half, all of them loaded by now
-        tc::tmem_st16(colS + c0 / 2, packed);
+      if (masks & 2) {
+        see &= same_document(st.doc[half * 64 + lane], st.doc[half * 64 + 32 + lane], my_doc);
+        if (!key_ok) see = 0ull;
       }
+      const bool hidden = __any_sync(0xffffffffu, see != ~0ull);
+      if (hidden) probs(std::true_type{}); else probs(std::false_type{});
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -406,27 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc::fence_after_sync();
-#pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t dp[32], packed[16];
-        tc::tmem_ld32(colP + c0, dp);
-        tc::tmem_ld_wait();
-        const uint32_t bits = (uint32_t)(see >> c0);
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 d4 = *reinterpret_cast<const float4*>(&st.delta[half * 64 + c0 + c]);
-          const float d[4] = {d4.x, d4.y, d4.z, d4.w};
-          float ds[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ds[e] = pw[c0 + c + e] * (__uint_as_float(dp[c + e]) - d[e]);
-            if (!((bits >> (c + e)) & 1u)) ds[e] = 0.f;       // dP of a masked pair may be anything
-          }
-          packed[c / 2] = pack_bf16(ds[0], ds[1]);
-          packed[c / 2 + 1] = pack_bf16(ds[2], ds[3]);
-        }
-        tc::tmem_st16(colP + c0 / 2, packed);
-      }
+      if (hidden) grads(std::true_type{}); else grads(std::false_type{});
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -492,7 +513,8 @@ template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                       const DenseArgs a, const int qpt) {
+                       const DenseArgs a, const int qpt,
+                       const TileOrder order) {
   using L = DqLayout<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -500,7 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   DqBars* bars = reinterpret_cast<DqBars*>(smem + L::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
-  const int t = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;      // the longest tiles first
+  int x, bh;
+  tile_of(order, blockIdx.x, x, bh);
+  const int t = order.tiles - 1 - x, b = bh / a.Hkv, h = bh - b * a.Hkv;      // the longest tiles first
   const int i0 = t * qpt, i1 = min(i0 + qpt, a.Sq);
   const DenseSeq seq = dense_seq(a, b);
   const int32_t* doc_q = a.mask.doc_q != nullptr ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
@@ -660,51 +684,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       lse2 = a.lse[flat] * kLog2e;
       delta = a.delta[flat];
     }
-    const float cap2 = a.cap * kLog2e, in = CAP ? a.scale / a.cap * (2.f * kLog2e) : 0.f, scale2 = a.scale * kLog2e;
-    const float slope2 = row.slope * kLog2e;
-    bool ok = true;
+    const ScoreMap<CAP, BIAS> map(a, row);
+    const uint64_t after2 = f2(map.after, map.after), nlse2 = f2(-lse2, -lse2), ndelta2 = f2(-delta, -delta);
+    uint64_t pw[32];       // P, then P times the cap's derivative, in pairs
+    uint64_t see = ~0ull;  // bit c: this lane's row sees key c of this half
     uint32_t g = 0;
-    for (int j; (j = walk.next(lane)) >= 0; ++g) {
-      const uint32_t colS = tbase + lanes + (g & 1 ? kColB : kColA) + half * 64;
-      const uint32_t colP = tbase + lanes + L::kColDp + half * 64;
-      const int first = j * kT + half * 64;
-      if (!warp_wait(&bars->s_full[g & 1], (g >> 1) & 1, abort)) {
-        fail(&bars->abort, 10);
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();
-      float pw[64];
-      const uint64_t see = visible64(row, doc_k, doc_k != nullptr ? walk.docs[j] : make_int2(0, 0), first);
-      const float far = (float)(row.pos - first);
+    const uint32_t colP = tbase + lanes + L::kColDp + half * 64;
+
+    auto probs = [&](auto masked, uint32_t colS, int far) {
+      constexpr bool MASK = decltype(masked)::value;
 #pragma unroll
       for (int c0 = 0; c0 < 64; c0 += 32) {
         uint32_t s[32];
         tc::tmem_ld32(colS + c0, s);
         tc::tmem_ld_wait();
+        if (CAP) {
+          tanh32(s, map.in);
+          if (BIAS) {                         // the derivative's factor, before the bias takes t's place
+#pragma unroll
+            for (int c = 0; c < 32; c += 2)
+              pw[(c0 + c) / 2] = f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          }
+        }
+        if (BIAS) map.bias(s, far - c0);
         const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float x = __uint_as_float(s[c]);
-          float y, dcap = 1.f;
-          if (CAP) {
-            const float th = fmaf(-2.f, rcp(1.f + ex2(x * in)), 1.f);
-            y = fmaf(cap2, th, -lse2);
-            dcap = fmaf(-th, th, 1.f);
-          } else {
-            y = fmaf(x, scale2, -lse2);
+        for (int c = 0; c < 32; c += 2) {
+          const uint64_t t2 = f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          float y0, y1;
+          f2_split(ffma2(t2, after2, nlse2), y0, y1);
+          float p0 = ex2(y0), p1 = ex2(y1);
+          if (MASK) {
+            p0 = (bits >> c) & 1u ? p0 : 0.f;
+            p1 = (bits >> (c + 1)) & 1u ? p1 : 0.f;
           }
-          if (BIAS) y = fmaf(-slope2, fabsf(far - (float)(c0 + c)), y);
-          const float p = (bits >> c) & 1u ? ex2(y) : 0.f;
-          pw[c0 + c] = CAP ? p * dcap : p;
+          pw[(c0 + c) / 2] = CAP ? times_dcap(f2(p0, p1), BIAS ? pw[(c0 + c) / 2] : t2) : f2(p0, p1);
         }
       }
-      if (!warp_wait(&bars->dp_full, g & 1, abort)) {
-        fail(&bars->abort, 11);
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();
+    };
+    // dS over the scores of this half, which are in registers
+    auto grads = [&](auto masked, uint32_t colS) {
+      constexpr bool MASK = decltype(masked)::value;
 #pragma unroll
       for (int c0 = 0; c0 < 64; c0 += 32) {
         uint32_t dp[32], packed[16];
@@ -713,14 +733,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          float d0 = pw[c0 + c] * (__uint_as_float(dp[c]) - delta);
-          float d1 = pw[c0 + c + 1] * (__uint_as_float(dp[c + 1]) - delta);
-          if (!((bits >> c) & 1u)) d0 = 0.f;            // dP of a masked pair may be anything
-          if (!((bits >> (c + 1)) & 1u)) d1 = 0.f;
+          float d0, d1;
+          f2_split(fmul2(pw[(c0 + c) / 2], fadd2(f2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), ndelta2)), d0, d1);
+          if (MASK) {                         // dP of a hidden pair may be anything
+            d0 = (bits >> c) & 1u ? d0 : 0.f;
+            d1 = (bits >> (c + 1)) & 1u ? d1 : 0.f;
+          }
           packed[c / 2] = pack_bf16(d0, d1);
         }
-        tc::tmem_st16(colS + c0 / 2, packed);           // over the scores of this half, which are in registers
+        tc::tmem_st16(colS + c0 / 2, packed);
       }
+    };
+
+    bool ok = true;
+    for (int j; (j = walk.next(lane)) >= 0; ++g) {
+      const uint32_t colS = tbase + lanes + (g & 1 ? kColB : kColA) + half * 64;
+      const int first = j * kT + half * 64;
+      if (!warp_wait(&bars->s_full[g & 1], (g >> 1) & 1, abort)) {
+        fail(&bars->abort, 10);
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      see = visible64(row, doc_k, doc_k != nullptr ? walk.docs[j] : make_int2(0, 0), first, a.Sk, lane);
+      const bool hidden = __any_sync(0xffffffffu, see != ~0ull);
+      if (hidden) probs(std::true_type{}, colS, row.pos - first); else probs(std::false_type{}, colS, row.pos - first);
+      if (!warp_wait(&bars->dp_full, g & 1, abort)) {
+        fail(&bars->abort, 11);
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      if (hidden) grads(std::true_type{}, colS); else grads(std::false_type{}, colS);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -770,7 +814,9 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
     const size_t smem = imax<size_t>(DkvLayout<D>::kBytes + 1024, kAloneBytes);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3((unsigned)((a.Sk + kT - 1) / kT), a.Hkv, a.B), kThreads, smem, st>>>(mq, mg, mk, mv, a, qpt);
+    const TileOrder order = tile_order(a, (a.Sk + kT - 1) / kT, a.causal);
+    if ((int64_t)order.tiles * order.heads > 0x7fffffff) return cudaErrorInvalidValue;
+    kernel<<<order.tiles * order.heads, kThreads, smem, st>>>(mq, mg, mk, mv, a, qpt, order);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -778,7 +824,9 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   const size_t smem = imax<size_t>(DqLayout<D>::kBytes + 1024, kAloneBytes);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3((unsigned)((a.Sq + qpt - 1) / qpt), a.Hkv, a.B), kThreads, smem, st>>>(mq, mg, mk, mv, a, qpt);
+  const TileOrder order = tile_order(a, (a.Sq + qpt - 1) / qpt, a.causal);
+  if ((int64_t)order.tiles * order.heads > 0x7fffffff) return cudaErrorInvalidValue;
+  kernel<<<order.tiles * order.heads, kThreads, smem, st>>>(mq, mg, mk, mv, a, qpt, order);
   return cudaGetLastError();
 }
 

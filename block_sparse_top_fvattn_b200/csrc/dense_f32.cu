@@ -33,6 +33,21 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
                      __uint_as_float(v.y & 0xffff0000u));
 }
 
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = load4(p), b = load4(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
 template <int D>
 struct Tile {
   static constexpr int kLd = D + 4;        // rows of a tile 16 bytes apart in the banks
@@ -274,26 +289,34 @@ __global__ void __launch_bounds__(kThreads) dense_combine_kernel(const DenseArgs
   if (lane == 0 && a.lse != nullptr) a.lse[flat] = total == 0.f ? -INFINITY : m + logf(total);
 }
 
-// delta = sum_d (out + rest) dout, one warp per row. Padding queries get 0, whatever they hold.
+// delta = sum_d (out + rest) dout; eight elements per lane, d / 8 lanes per row. Padding queries get 0,
+// whatever they hold.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) dense_delta_kernel(const DenseArgs a) {
+  constexpr int LPR = D / 8;
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
-  const int64_t flat = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (flat >= rows) return;
-  const int64_t iq = flat % a.Sq, bh = flat / a.Sq, b = bh / a.Hq, hq = bh - b * a.Hq;
-  constexpr int N = D / 32;
-  const int64_t at = b * a.os.b + hq * a.os.h + iq * a.os.s + lane * N;
-  const T* o = static_cast<const T*>(a.out) + at;
-  const T* r = a.rest != nullptr ? static_cast<const T*>(a.rest) + at : nullptr;
-  const T* g = static_cast<const T*>(a.dout) + b * a.dos.b + hq * a.dos.h + iq * a.dos.s + lane * N;
+  const int64_t flat = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+  const int l = threadIdx.x % LPR;
   float acc = 0.f;
+  if (flat < rows) {
+    const int64_t iq = flat % a.Sq, bh = flat / a.Sq, b = bh / a.Hq, hq = bh - b * a.Hq;
+    const int64_t at = b * a.os.b + hq * a.os.h + iq * a.os.s + l * 8;
+    float o[8], g[8];
+    load8(static_cast<const T*>(a.out) + at, o);
+    load8(static_cast<const T*>(a.dout) + b * a.dos.b + hq * a.dos.h + iq * a.dos.s + l * 8, g);
+    if (a.rest != nullptr) {
+      float r[8];
+      load8(static_cast<const T*>(a.rest) + at, r);
 #pragma unroll
-  for (int c = 0; c < N; ++c) acc = fmaf(to_f32(o[c]) + (r != nullptr ? to_f32(r[c]) : 0.f), to_f32(g[c]), acc);
+      for (int c = 0; c < 8; ++c) o[c] += r[c];
+    }
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
-  const bool pad = a.mask.doc_q != nullptr && a.mask.doc_q[b * a.Sq + iq] < 0;
-  if (lane == 0) a.delta[flat] = pad ? 0.f : acc;
+    for (int c = 0; c < 8; ++c) acc = fmaf(o[c], g[c], acc);
+    if (a.mask.doc_q != nullptr && a.mask.doc_q[b * a.Sq + iq] < 0) acc = 0.f;
+  }
+#pragma unroll
+  for (int x = LPR / 2; x > 0; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
+  if (l == 0 && flat < rows) a.delta[flat] = acc;
 }
 
 // The documents of each block of `block` tokens of doc [B][S], one warp per block: x = the lowest
@@ -499,6 +522,10 @@ cudaError_t bwd_d(const DenseArgs& a, cudaStream_t st) {
   return run(dense_dkv_kernel<T, D>, dim3((unsigned)((a.Sk + kT - 1) / kT), a.Hkv, a.B), smem, a, st);
 }
 
+unsigned delta_blocks(const DenseArgs& a) {
+  const int64_t per = kThreads / (a.d / 8);
+  return (unsigned)(((int64_t)a.B * a.Hq * a.Sq + per - 1) / per);
+}
 unsigned warp_rows(const DenseArgs& a) {
   return (unsigned)(((int64_t)a.B * a.Hq * a.Sq + kThreads / 32 - 1) / (kThreads / 32));
 }
@@ -531,11 +558,11 @@ cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st)
 
 cudaError_t launch_dense_delta(const DenseArgs& a, int dtype, cudaStream_t st) {
   if (dtype == FVATTN_F32) {
-    if (a.d == 128) dense_delta_kernel<float, 128><<<warp_rows(a), kThreads, 0, st>>>(a);
-    else dense_delta_kernel<float, 64><<<warp_rows(a), kThreads, 0, st>>>(a);
+    if (a.d == 128) dense_delta_kernel<float, 128><<<delta_blocks(a), kThreads, 0, st>>>(a);
+    else dense_delta_kernel<float, 64><<<delta_blocks(a), kThreads, 0, st>>>(a);
   } else {
-    if (a.d == 128) dense_delta_kernel<__nv_bfloat16, 128><<<warp_rows(a), kThreads, 0, st>>>(a);
-    else dense_delta_kernel<__nv_bfloat16, 64><<<warp_rows(a), kThreads, 0, st>>>(a);
+    if (a.d == 128) dense_delta_kernel<__nv_bfloat16, 128><<<delta_blocks(a), kThreads, 0, st>>>(a);
+    else dense_delta_kernel<__nv_bfloat16, 64><<<delta_blocks(a), kThreads, 0, st>>>(a);
   }
   return cudaGetLastError();
 }

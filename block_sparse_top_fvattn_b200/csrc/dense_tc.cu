@@ -32,7 +32,7 @@ namespace fv {
 namespace {
 
 constexpr int NS = 2;          // stages of K and of V; the stage of a step is also its S / P buffer
-constexpr int kWarps = 7;      // K loader, MMA, four softmax warps, V loader
+constexpr int kWarps = 6;      // loader, MMA, four softmax warps
 constexpr float kRescaleLog2 = 8.0f;
 
 template <int D>
@@ -67,7 +67,8 @@ struct FwdBars {
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     dense_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const DenseArgs a, const int qpt) {
+                    const __grid_constant__ CUtensorMap tmV, const DenseArgs a, const int qpt,
+                    const TileOrder order) {
   using L = FwdLayout<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -79,9 +80,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
 
-  const int split = blockIdx.x % a.splits;
-  const int t = gridDim.x / a.splits - 1 - blockIdx.x / a.splits;     // the longest tiles first under an order
-  const int h = blockIdx.y, b = blockIdx.z;
+  int x, bh;
+  tile_of(order, blockIdx.x, x, bh);
+  const int split = x % a.splits, t = order.tiles / a.splits - 1 - x / a.splits;
+  const int b = bh / a.Hkv, h = bh - b * a.Hkv;
   const int i0 = t * qpt, i1 = min(i0 + qpt, a.Sq);                   // this tile's queries
   const DenseSeq seq = dense_seq(a, b);
   const int key0 = split * a.split_keys;
@@ -130,65 +132,60 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   BlockWalk walk(docs, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ Q and K loader
+    // ------------------------------------------------------------ loader
+    // K_g as soon as the S that read its stage is done, then V_{g-1} once the P V that read its is.
     int k_par[NS] = {-1, -1};
     bool q_armed = false;
-    uint32_t g = 0;
-    for (int j; (j = walk.next(lane)) >= 0; ++g) {
-      int ok = 1;
+    const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+    auto load_k = [&](uint32_t g, int j) -> bool {
+      const int st = g % NS;
+      if (!warp_wait(&bars->s_full[st], ((g / NS) & 1) ^ 1, abort)) return false;
       if (lane == 0) {
-        if (g == 0) {
-          tc::mbar_expect_tx(&bars->q_full, (uint32_t)(qpt * a.G) * 128 * (D / 64));
-          q_armed = true;
-          for (int c = 0; c < D / 64; ++c)
-            tc::tma_load_5d(sQ + c * L::kQChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
-        }
-        const int st = g % NS;
-        if (!tc::mbar_wait(&bars->s_full[st], ((g / NS) & 1) ^ 1, abort, kWaitLimit)) {
-          fail(&bars->abort, 3);
-          ok = 0;
-        } else {
-          tc::mbar_expect_tx(&bars->k_full[st], L::kKBytes);
-          k_par[st] = (g / NS) & 1;
-          for (int c = 0; c < D / 64; ++c)
-            tc::tma_load_4d(sK + st * L::kKBytes + c * L::kKVChunk, &tmK, &bars->k_full[st], c * 64, j * kBlock, h, b);
-        }
+        tc::mbar_expect_tx(&bars->k_full[st], L::kKBytes);
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_4d(sK + st * L::kKBytes + c * L::kKVChunk, &tmK, &bars->k_full[st], c * 64, j * kBlock, h, b);
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      k_par[0] = st == 0 ? (int)((g / NS) & 1) : k_par[0];
+      k_par[1] = st == 1 ? (int)((g / NS) & 1) : k_par[1];
+      return true;
+    };
+    auto load_v = [&](uint32_t g, int j) -> bool {
+      const int st = g % NS;
+      unsigned char* dst = sV + st * L::kKBytes;
+      if (!warp_wait(&bars->pv_done[st], ((g / NS) & 1) ^ 1, abort)) return false;
+      // keys that do not exist although their memory does: zeros, whatever it holds (0 * NaN would reach O)
+      if ((seq.kv < a.Sk && (j + 1) * kBlock > seq.kv) || (docs != nullptr && docs[j].x < 0)) {
+        copy_keys<D>(dst, static_cast<const __nv_bfloat16*>(a.v) + (int64_t)b * a.vs.b + (int64_t)h * a.vs.h, a.vs.s,
+                     j * kBlock, kBlock, seq.kv, doc_k, lane, 32);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->p_full[st]);
+      } else if (lane == 0) {
+        tc::mbar_expect_tx(&bars->p_full[st], L::kKBytes);
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_4d(dst + c * L::kKVChunk, &tmV, &bars->p_full[st], c * 64, j * kBlock, h, b);
+      }
+      if (lane == 0) *reinterpret_cast<volatile int*>(&bars->v_armed) = (int)g;
+      return true;
+    };
+    uint32_t g = 0;
+    int before = -1;
+    bool ok = true;
+    for (int j; ok && (j = walk.next(lane)) >= 0; ++g) {
+      if (g == 0 && lane == 0) {
+        tc::mbar_expect_tx(&bars->q_full, (uint32_t)(qpt * a.G) * 128 * (D / 64));
+        q_armed = true;
+        for (int c = 0; c < D / 64; ++c) tc::tma_load_5d(sQ + c * L::kQChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
+      }
+      ok = load_k(g, j) && (g == 0 || load_v(g - 1, before));
+      before = j;
     }
+    if (!ok || (g > 0 && !load_v(g - 1, before))) fail(&bars->abort, 3);
     // no copy may still be writing shared memory when the CTA leaves
     if (lane == 0) {
       if (q_armed) tc::mbar_wait_drain(&bars->q_full, 0, kWaitLimit);
       for (int st = 0; st < NS; ++st)
         if (k_par[st] >= 0) tc::mbar_wait_drain(&bars->k_full[st], (uint32_t)k_par[st], kWaitLimit);
-    }
-  } else if (warp == 6) {
-    // ------------------------------------------------------------ V loader
-    uint32_t g = 0;
-    for (int j; (j = walk.next(lane)) >= 0; ++g) {
-      const int st = g % NS;
-      if (!warp_wait(&bars->pv_done[st], ((g / NS) & 1) ^ 1, abort)) {
-        fail(&bars->abort, 16);
-        break;
-      }
-      unsigned char* dst = sV + st * L::kKBytes;
-      // keys that do not exist although their memory does: zeros, whatever it holds (0 * NaN would reach O)
-      if ((seq.kv < a.Sk && (j + 1) * kBlock > seq.kv) || (docs != nullptr && docs[j].x < 0)) {
-        copy_keys<D>(dst, static_cast<const __nv_bfloat16*>(a.v) + (int64_t)b * a.vs.b + (int64_t)h * a.vs.h, a.vs.s, j * kBlock, kBlock,
-                     seq.kv, a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr, lane, 32);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&bars->p_full[st]);
-          *reinterpret_cast<volatile int*>(&bars->v_armed) = (int)g;
-        }
-      } else if (lane == 0) {
-        tc::mbar_expect_tx(&bars->p_full[st], L::kKBytes);
-        for (int c = 0; c < D / 64; ++c)
-          tc::tma_load_4d(dst + c * L::kKVChunk, &tmV, &bars->p_full[st], c * 64, j * kBlock, h, b);
-        *reinterpret_cast<volatile int*>(&bars->v_armed) = (int)g;
-      }
-      __syncwarp();
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -269,24 +266,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       }
       if (live_warp) {
         tc::fence_after_sync();
-        uint32_t sraw[64];
-        {
-          uint32_t (&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sraw[0]);
-          uint32_t (&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sraw[32]);
-          tc::tmem_ld32(sp, lo);
-          tc::tmem_ld32(sp + 32, hi);
-          tc::tmem_ld_wait();
-        }
-        map.template apply<64>(sraw, row.pos - j * kBlock);
-        const uint64_t see = visible64(row, doc_k, docs != nullptr ? docs[j] : make_int2(0, 0), j * kBlock);
+        uint32_t lo[32], hi[32];
+        tc::tmem_ld32(sp, lo);
+        tc::tmem_ld32(sp + 32, hi);
+        tc::tmem_ld_wait();
+        map.apply(lo, row.pos - j * kBlock);
+        map.apply(hi, row.pos - j * kBlock - 32);
+        const uint64_t see = visible64(row, doc_k, docs != nullptr ? docs[j] : make_int2(0, 0), j * kBlock, a.Sk, lane);
         if (__any_sync(0xffffffffu, see != ~0ull)) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            if (!(((uint32_t)see >> c) & 1u)) sraw[c] = __float_as_uint(-INFINITY);
-            if (!(((uint32_t)(see >> 32) >> c) & 1u)) sraw[32 + c] = __float_as_uint(-INFINITY);
+            if (!(((uint32_t)see >> c) & 1u)) lo[c] = __float_as_uint(-INFINITY);
+            if (!(((uint32_t)(see >> 32) >> c) & 1u)) hi[c] = __float_as_uint(-INFINITY);
           }
         }
-        const float mx = max64(sraw) * map.after;
+        const float mx = fmaxf(max32(lo), max32(hi)) * map.after;
         const bool raise = mrow == -INFINITY || mx > mrow + kRescaleLog2;
         const bool scale_o = raise && g > 0 && mrow != -INFINITY;
         if (__any_sync(0xffffffffu, scale_o)) {
@@ -319,15 +313,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         const uint64_t negm = f2(nm, nm), after2 = f2(map.after, map.after);
         uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
         uint32_t packed[32];
+        auto weights = [&](const uint32_t (&x)[32], int at) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const uint64_t x2 = ffma2(f2(__uint_as_float(sraw[2 * c]), __uint_as_float(sraw[2 * c + 1])), after2, negm);
-          float x0, x1;
-          f2_split(x2, x0, x1);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          acc[c & 3] = fadd2(acc[c & 3], f2(p0, p1));
-          packed[c] = pack_bf16(p0, p1);
-        }
+          for (int c = 0; c < 16; ++c) {
+            const uint64_t x2 = ffma2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), after2, negm);
+            float x0, x1;
+            f2_split(x2, x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            acc[c & 3] = fadd2(acc[c & 3], f2(p0, p1));
+            packed[at + c] = pack_bf16(p0, p1);
+          }
+        };
+        weights(lo, 0);
+        weights(hi, 16);
         lsum = fadd2(lsum, fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])));
         tc::tmem_st32(sp, packed);           // S_g is in registers
         tc::tmem_st_wait();
@@ -419,8 +417,10 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   auto* kernel = dense_tc_kernel<D, CAP, BIAS>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const unsigned tiles = (unsigned)((a.Sq + qpt - 1) / qpt);
-  kernel<<<dim3(tiles * a.splits, a.Hkv, a.B), kWarps * 32, smem, st>>>(mq, mk, mv, a, qpt);
+  const TileOrder order = tile_order(a, (a.Sq + qpt - 1) / qpt * a.splits, a.causal);
+  const int64_t grid = (int64_t)order.tiles * order.heads;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  kernel<<<(unsigned)grid, kWarps * 32, smem, st>>>(mq, mk, mv, a, qpt, order);
   return cudaGetLastError();
 }
 

@@ -63,14 +63,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
-  float m[21];
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float m[11];
 #pragma unroll
-  for (int c = 0; c < 21; ++c)
+  for (int c = 0; c < 10; ++c)
     m[c] = max3(__uint_as_float(s[3 * c]), __uint_as_float(s[3 * c + 1]), __uint_as_float(s[3 * c + 2]));
-#pragma unroll
-  for (int c = 0; c < 7; ++c) m[c] = max3(m[3 * c], m[3 * c + 1], m[3 * c + 2]);
-  return max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], __uint_as_float(s[63])));
+  m[10] = fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31]));
+  return max3(max3(max3(m[0], m[1], m[2]), m[3], m[4]), max3(m[5], m[6], m[7]), max3(m[8], m[9], m[10]));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -137,53 +136,149 @@ struct BlockWalk {
   }
 };
 
-// Bit c: key first + c is visible to the row; v: the documents of the block it lies in.
-__device__ __forceinline__ uint64_t visible64(const DenseRow& row, const int32_t* doc_k, int2 v, int first) {
-  const int n = row.limit - first;
-  uint64_t see = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+// Bits of the lower n of 64 (n may be negative or above 64).
+__device__ __forceinline__ uint64_t low64(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull; }
+
+// For a warp whose lanes hold 64 document numbers (d0, d1: tokens lane and lane + 32) and one of their
+// own: bit c of the result says that token c has this lane's. One round per distinct number among
+// the lanes, which is one or two where documents are runs of tokens. The whole warp takes part.
+__device__ __forceinline__ uint64_t same_document(int d0, int d1, int mine) {
+  uint64_t same = 0ull;
+  uint32_t left = 0xffffffffu;
+  while (left != 0u) {
+    const int d = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+    const uint32_t lo = __ballot_sync(0xffffffffu, d0 == d), hi = __ballot_sync(0xffffffffu, d1 == d);
+    if (mine == d) same = (uint64_t)hi << 32 | lo;
+    left &= ~__ballot_sync(0xffffffffu, mine == d);
+  }
+  return same;
+}
+
+// Bit c: key first + c is visible to this lane's row; v: the documents of the block it lies in. The
+// whole warp takes part.
+__device__ __forceinline__ uint64_t visible64(const DenseRow& row, const int32_t* doc_k, int2 v, int first, int Sk,
+                                              int lane) {
+  uint64_t see = low64(row.limit - first);
   if (doc_k != nullptr) {
     if (doc_uniform(v)) {
       if (v.y != row.doc) see = 0ull;
-    } else if (see != 0ull) {
-      // bits of keys at or past Sk are clear already: their document numbers are not read
-      uint64_t same = 0ull;
-      for (int c = 0; c < 64; ++c)
-        if ((see >> c) & 1ull) same |= (uint64_t)(doc_k[first + c] == row.doc) << c;
-      see &= same;
+    } else {
+      const int d0 = first + lane < Sk ? doc_k[first + lane] : -1;
+      const int d1 = first + 32 + lane < Sk ? doc_k[first + 32 + lane] : -1;
+      see &= same_document(d0, d1, row.doc);      // a padding row's limit is 0
     }
   }
   return see;
 }
 
-// The score of a raw product x, up to the factor `after` that takes it to base-2 exponents:
-// x itself (after = scale log2 e), or the capped and biased score (after = log2 e).
+// tanh on pairs, |y| <= 1: y times a polynomial of degree 6 in y^2, fitted to the least largest error
+// (2e-8; 1e-7 with fp32 arithmetic). On the FMA pipe: the exponentials of the softmax already fill the
+// SFU, and tanh by exponential and reciprocal would triple its work.
+__device__ __forceinline__ uint64_t tanh_small2(uint64_t y) {
+  const uint64_t u = fmul2(y, y);
+  uint64_t p = f2(0.0009637684561312199f, 0.0009637684561312199f);
+  p = ffma2(p, u, f2(-0.005951268598437309f, -0.005951268598437309f));
+  p = ffma2(p, u, f2(0.01997326873242855f, 0.01997326873242855f));
+  p = ffma2(p, u, f2(-0.05326582491397858f, -0.05326582491397858f));
+  p = ffma2(p, u, f2(0.13319583237171173f, 0.13319583237171173f));
+  p = ffma2(p, u, f2(-0.33332130312919617f, -0.33332130312919617f));
+  p = ffma2(p, u, f2(0.9999997019767761f, 0.9999997019767761f));
+  return fmul2(p, y);
+}
+// tanh(y) = 1 - 2 / (1 + e^2y) for any y, off by a few 2^-24; e^2y at inf or 0 gives 1 and -1.
+__device__ __forceinline__ float tanh_any(float y) {
+  return fmaf(-2.f, rcp(1.f + ex2(y * (2.f * kLog2e))), 1.f);
+}
+__device__ __forceinline__ float abs_max32(const uint32_t (&s)[32]) {
+  float m = 0.f;
+#pragma unroll
+  for (int c = 0; c < 32; c += 2)
+    m = max3(m, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+  return m;
+}
+
+// s <- tanh(s * in), the polynomial where every score of the warp allows it. The whole warp takes part.
+__device__ __forceinline__ void tanh32(uint32_t (&s)[32], float in) {
+  if (__all_sync(0xffffffffu, abs_max32(s) * in <= 1.f)) {
+    const uint64_t in2 = f2(in, in);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      float a, b;
+      f2_split(tanh_small2(fmul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), in2)), a, b);
+      s[c] = __float_as_uint(a);
+      s[c + 1] = __float_as_uint(b);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(tanh_any(__uint_as_float(s[c]) * in));
+  }
+}
+
+// The score of a raw product, a row per lane: `apply` leaves values that `after` takes to base-2
+// exponents (products, after = scale log2 e; tanh, after = cap log2 e; biased exponents, after = 1).
 template <bool CAP, bool BIAS>
 struct ScoreMap {
-  float scale, after, cap, in, slope;
+  float in, factor, after, slope2;
   __device__ __forceinline__ ScoreMap(const DenseArgs& a, const DenseRow& row) {
-    scale = a.scale;
-    cap = a.cap;
-    after = (CAP || BIAS) ? kLog2e : a.scale * kLog2e;
-    in = CAP ? a.scale / a.cap * (2.f * kLog2e) : 0.f;
-    slope = row.slope;
+    in = CAP ? a.scale / a.cap : 0.f;
+    factor = (CAP ? a.cap : a.scale) * kLog2e;
+    after = BIAS ? 1.f : factor;
+    slope2 = row.slope * kLog2e;
   }
-  // tanh(y) = 1 - 2 / (1 + e^2y), off by a few 2^-24 absolutely: with the scaled product that is a few
-  // 2^-24 of the cap. e^2y overflowing to inf or vanishing gives 1 and -1.
-  __device__ __forceinline__ float tanh_of(float x) const { return fmaf(-2.f, rcp(1.f + ex2(x * in)), 1.f); }
-  // N scores in place; `far` = position of the row minus the first key.
-  template <int N>
-  __device__ __forceinline__ void apply(uint32_t (&s)[N], int far) const {
-    if (!CAP && !BIAS) return;
+  // 32 scores in place; far = position of the row minus the first key. The whole warp takes part.
+  __device__ __forceinline__ void apply(uint32_t (&s)[32], int far) const {
+    if (CAP) tanh32(s, in);
+    if (BIAS) bias(s, far);
+  }
+  __device__ __forceinline__ void bias(uint32_t (&s)[32], int far) const {
     const float f = (float)far;
+    const bool past = __all_sync(0xffffffffu, far >= 31), ahead = __all_sync(0xffffffffu, far <= 0);
+    if (past || ahead) {
+      // all keys on one side of every row: the bias is linear in the key
+      const float k1 = past ? slope2 : -slope2, k0 = -k1 * f;
+      const uint64_t k12 = f2(k1, k1), k02 = f2(k0, k0), factor2 = f2(factor, factor);
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      float x = __uint_as_float(s[c]);
-      x = CAP ? cap * tanh_of(x) : x * scale;
-      if (BIAS) x = fmaf(-slope, fabsf(f - (float)c), x);
-      s[c] = __float_as_uint(x);
+      for (int c = 0; c < 32; c += 2) {
+        float x, y;
+        f2_split(ffma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), factor2,
+                       ffma2(k12, f2((float)c, (float)(c + 1)), k02)), x, y);
+        s[c] = __float_as_uint(x);
+        s[c + 1] = __float_as_uint(y);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        s[c] = __float_as_uint(fmaf(-slope2, fabsf(f - (float)c), __uint_as_float(s[c]) * factor));
     }
   }
 };
+
+// p times the cap's derivative 1 - t^2, in pairs.
+__device__ __forceinline__ uint64_t times_dcap(uint64_t p, uint64_t t) {
+  const uint64_t tt = fmul2(fmul2(t, f2(-1.f, -1.f)), t);
+  return ffma2(p, tt, p);
+}
+
+// Which tile a CTA takes. Under an order the tiles of a head differ in length and the longest should
+// start first, over all heads; but the heads in flight share L2, so heads go in groups whose keys fit
+// half of it. Otherwise a head's tiles run next to one another.
+struct TileOrder {
+  int group;       // key heads (over the batch) per group
+  int tiles;       // tiles (or tiles x splits) per key head
+  int heads;       // B * Hkv
+};
+__device__ __forceinline__ void tile_of(const TileOrder& o, int64_t x, int& tile, int& bh) {
+  const int64_t per = (int64_t)o.group * o.tiles;
+  const int grp = (int)(x / per), rest = (int)(x - grp * per);
+  const int n = min(o.group, o.heads - grp * o.group);
+  tile = rest / n;
+  bh = grp * o.group + rest % n;
+}
+inline TileOrder tile_order(const DenseArgs& a, int tiles, bool longest_first) {
+  const int64_t heads = (int64_t)a.B * a.Hkv, bytes = (int64_t)(longest_first ? a.Sk : 1) * a.d * 4;
+  const int64_t fit = imax<int64_t>(1, (int64_t)(60 << 20) / bytes);
+  return TileOrder{longest_first ? (int)imin(heads, fit) : 1, tiles, (int)heads};
+}
 
 // `rows` tokens from token t0 of a [token][D] matrix into a tile of 128-byte swizzled rows (chunks of 64
 // dims), zeros for tokens at or past `end` and for padding documents; lanes `me` of `of`.
