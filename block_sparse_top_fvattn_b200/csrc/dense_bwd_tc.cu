@@ -10,7 +10,7 @@
 // gradient is summed over its query heads in TMEM.
 //
 // dK, dV: scores transposed (lane = key, column = row), so that P^T and dS^T are written over the
-// scores in TMEM as the first operands of their products. Per tile, with eight warps between them:
+// scores in TMEM as the first operands of their products. Per tile, with sixteen warps between them:
 //   products   dV(i) S(i+1)            | dK(i) dP(i+1)
 //   warps      dS(i) from dP(i), P(i)  | P(i+1) from S(i+1)
 // dQ: lane = row; S has two buffers, so S(i+1) is ready when dS(i) is done:
@@ -36,7 +36,10 @@ namespace fv {
 namespace {
 
 constexpr int kT = 128;               // rows and keys of a tile
-constexpr int kWarps = 10;            // loader, MMA, eight for the elementwise work
+constexpr int kWarps = 18;            // loader, MMA, sixteen for the elementwise work: four per scheduler,
+                                      // which hide one another's waits for TMEM and the SFU
+constexpr int kWork = 16;
+constexpr int kCols = kT * 4 / kWork; // columns of a score tile per thread
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kColA = 0;         // scores (dQ: their first buffer)
 constexpr uint32_t kColB = 128;       // dP (dQ: the scores' second buffer)
@@ -63,14 +66,14 @@ __device__ __forceinline__ void mma_dims(uint32_t d_tmem, uint32_t a_addr, uint3
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) tc::mma_f16(d_tmem, desc_dims(a_addr, kk), desc_dims(b_addr, kk), id, kk > 0);
 }
-// D[128 x D] (+)= W B over the 128 tokens of a tile, W (bf16) in TMEM: the first 64 tokens at w, the
-// others 64 columns further, each half over the fp32 values it was made from.
+// D[128 x D] (+)= W B over the 128 tokens of a tile, W (bf16) in TMEM: every kCols tokens over the fp32
+// values they were made from.
 template <int D>
 __device__ __forceinline__ void mma_tokens(uint32_t d_tmem, uint32_t w, uint32_t b_addr, bool add) {
   constexpr uint32_t id = tc::idesc_bf16_f32(kT, D, 0, 1);
 #pragma unroll
   for (int kk = 0; kk < kT / 16; ++kk)
-    tc::mma_f16_tmem_a(d_tmem, w + (kk >> 2) * 64 + (kk & 3) * 8, desc_tokens(b_addr, kk), id, add || kk > 0);
+    tc::mma_f16_tmem_a(d_tmem, w + (kk / (kCols / 16)) * kCols + (kk % (kCols / 16)) * 8, desc_tokens(b_addr, kk), id, add || kk > 0);
 }
 
 // 32 fp32 results, times `by`, as bf16.
@@ -104,12 +107,10 @@ struct DkvLayout : BwdLayout<D> {
 
 struct DkvBars {
   uint64_t kv_full;
-  uint64_t q_full[2], q_empty[2];     // Q and the row statistics of a tile
+  uint64_t q_full[2], q_empty[2];     // Q of a tile
   uint64_t g_full[2], g_empty[2];     // dout of a tile
   uint64_t s_full, p_full, dp_full, ds_full;
   uint64_t drain;
-  int rows[2];                        // rows of the tile that are queries; the others come last
-  int masks[2];                       // whether limits (1) or documents (2) hide pairs of those rows
   int doc_lo, doc_hi, doc_pad;        // documents of the keys
   uint32_t tmem_base;
   int abort;
@@ -140,15 +141,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->kv_full, 1);
     for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(&bars->q_full[s], 2);      // the copy (or its stand-in), the statistics
+      tc::mbar_init(&bars->q_full[s], 1);
       tc::mbar_init(&bars->q_empty[s], 1);
       tc::mbar_init(&bars->g_full[s], 1);
       tc::mbar_init(&bars->g_empty[s], 1);
     }
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->p_full, 8);
-    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->p_full, kWork);
+    tc::mbar_init(&bars->ds_full, kWork);
     tc::mbar_init(&bars->drain, 1);
     bars->abort = 0;
     bars->doc_lo = 0x7fffffff;
@@ -206,7 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     const uint32_t bytes = (uint32_t)(qpt * a.G) * 128 * (D / 64);
-    const int jend = min(kT, seq.kv - j0);
     uint32_t g = 0;
     for (int t; (t = walk.next(lane)) >= 0; ++g) {
       const int s = g & 1;
@@ -232,39 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&bars->q_full[s]);
       }
       q_par[s] = (int)par;
-      // row statistics
-      RowStats& st = stats[s];
-      const int rows = min(qpt, a.Sq - i0) * a.G;
-      bool limits = false, docs = false;
-#pragma unroll
-      for (int u = 0; u < kT / 32; ++u) {
-        const int r = u * 32 + lane;
-        DenseRow row{0, -1, 0, 0.f};
-        float lse = 0.f, delta = 0.f;
-        if (r < rows) {
-          const int i = i0 + r / a.G, hq = h * a.G + r % a.G;
-          row = dense_row(a, seq, b, hq, i);
-          const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + i;
-          lse = a.lse[flat];
-          delta = a.delta[flat];
-          limits = limits || row.limit - j0 < jend;
-          docs = docs || (doc_q != nullptr && row.doc != bars->doc_lo);
-        }
-        st.nlse2[r] = -lse * kLog2e;
-        st.ndelta[r] = -delta;
-        st.far[r] = (float)(row.pos - j0);
-        st.slope2[r] = row.slope * kLog2e;
-        st.limit[r] = row.limit - j0;
-        st.doc[r] = row.doc;
-      }
-      limits = __any_sync(0xffffffffu, limits);
-      docs = __any_sync(0xffffffffu, docs) || (doc_k != nullptr && (bars->doc_lo != bars->doc_hi || bars->doc_pad));
-      if (lane == 0) {
-        bars->rows[s] = rows;
-        bars->masks[s] = (limits ? 1 : 0) | (docs ? 2 : 0);
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->q_full[s]);
       if (!warp_wait(&bars->g_empty[s], par ^ 1, abort)) {
         fail(&bars->abort, 4);
         break;
@@ -334,142 +301,184 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ elementwise
-    const int q = warp & 3, half = (warp - 2) >> 2;      // TMEM lane quarter; first or second 64 rows of a tile
+    const int q = warp & 3, col0 = ((warp - 2) >> 2) * kCols;      // TMEM lane quarter, rows of a tile
     const int r = q * 32 + lane, j = j0 + r;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const uint32_t colS = tbase + lanes + kColA + half * 64, colP = tbase + lanes + kColB + half * 64;
+    const uint32_t colS = tbase + lanes + kColA + col0, colP = tbase + lanes + kColB + col0;
     const int my_doc = doc_k != nullptr && j < a.Sk ? doc_k[j] : 0;
     const bool key_ok = j < seq.kv && my_doc >= 0;
     const float in = CAP ? a.scale / a.cap : 0.f, factor = (CAP ? a.cap : a.scale) * kLog2e, fr = (float)r;
     const uint64_t factor2 = f2(factor, factor);
-    uint64_t pw[32];       // P, then P times the cap's derivative, in pairs
-    uint64_t see = ~0ull;  // bit c: row c of this half sees this lane's key
+    uint64_t pw[kCols / 2];          // P, then P times the cap's derivative, in pairs
+    uint32_t see = 0xffffffffu;      // bit c: row c of this warp's sees this lane's key
     uint32_t g = 0;
 
-    // P^T of this half's rows over the scores it is made from (columns 0-31 of the half, loaded by then)
+    // The row statistics of a tile: these threads hold one value each of the next tile's in flight, and
+    // write it at the start of its turn.
+    const int part = (threadIdx.x - 64) / kT, sr = (threadIdx.x - 64) % kT;
+    float ahead0 = 0.f, ahead1 = 0.f;
+    auto fetch = [&](int t) {
+      const int i0 = t * qpt, i = i0 + sr / a.G, hq = h * a.G + sr % a.G;
+      const bool row_ok = sr < min(qpt, a.Sq - i0) * a.G;
+      const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + i;
+      if (part == 0) {
+        ahead0 = row_ok ? -a.lse[flat] * kLog2e : 0.f;
+      } else if (part == 1) {
+        ahead0 = row_ok ? -a.delta[flat] : 0.f;
+      } else {
+        DenseRow row{0, -1, 0, 0.f};
+        if (row_ok) row = dense_row(a, seq, b, hq, i);
+        ahead0 = part == 2 ? __int_as_float(row.limit - j0) : (float)(row.pos - j0);
+        ahead1 = part == 2 ? __int_as_float(row.doc) : row.slope * kLog2e;
+      }
+    };
+    auto put = [&](RowStats& st) {
+      if (part == 0) {
+        st.nlse2[sr] = ahead0;
+      } else if (part == 1) {
+        st.ndelta[sr] = ahead0;
+      } else if (part == 2) {
+        st.limit[sr] = __float_as_int(ahead0);
+        st.doc[sr] = __float_as_int(ahead1);
+      } else {
+        st.far[sr] = ahead0;
+        st.slope2[sr] = ahead1;
+      }
+    };
+
+    // P^T of this warp's rows over the scores it is made from, loaded by then
     auto probs = [&](auto masked) {
       constexpr bool MASK = decltype(masked)::value;
       const RowStats& st = stats[g & 1];
+      uint32_t s[32], packed[16];
+      tc::tmem_ld32(colS, s);
+      tc::tmem_ld_wait();
+      if (CAP) tanh32(s, in);
 #pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t s[32], packed[16];
-        tc::tmem_ld32(colS + c0, s);
-        tc::tmem_ld_wait();
-        if (CAP) tanh32(s, in);
-        const uint32_t bits = (uint32_t)(see >> c0);
+      for (int c = 0; c < 32; c += 4) {
+        const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(&st.nlse2[col0 + c]);
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const int at = half * 64 + c0 + c;
-          const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(&st.nlse2[at]);
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const uint64_t t2 = f2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1]));
-            float y0, y1;
-            f2_split(ffma2(t2, factor2, e == 0 ? l4.x : l4.y), y0, y1);
-            if (BIAS) {
-              y0 = fmaf(-st.slope2[at + e], fabsf(st.far[at + e] - fr), y0);
-              y1 = fmaf(-st.slope2[at + e + 1], fabsf(st.far[at + e + 1] - fr), y1);
-            }
-            float p0 = ex2(y0), p1 = ex2(y1);
-            if (MASK) {
-              p0 = (bits >> (c + e)) & 1u ? p0 : 0.f;
-              p1 = (bits >> (c + e + 1)) & 1u ? p1 : 0.f;
-            }
-            packed[(c + e) / 2] = pack_bf16(p0, p1);
-            pw[(c0 + c + e) / 2] = CAP ? times_dcap(f2(p0, p1), t2) : f2(p0, p1);
+        for (int e = 0; e < 4; e += 2) {
+          const uint64_t t2 = f2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1]));
+          float y0, y1;
+          f2_split(ffma2(t2, factor2, e == 0 ? l4.x : l4.y), y0, y1);
+          if (BIAS) {
+            const int at = col0 + c + e;
+            y0 = fmaf(-st.slope2[at], fabsf(st.far[at] - fr), y0);
+            y1 = fmaf(-st.slope2[at + 1], fabsf(st.far[at + 1] - fr), y1);
           }
+          float p0 = ex2(y0), p1 = ex2(y1);
+          if (MASK) {
+            p0 = (see >> (c + e)) & 1u ? p0 : 0.f;
+            p1 = (see >> (c + e + 1)) & 1u ? p1 : 0.f;
+          }
+          packed[(c + e) / 2] = pack_bf16(p0, p1);
+          pw[(c + e) / 2] = CAP ? times_dcap(f2(p0, p1), t2) : f2(p0, p1);
         }
-        tc::tmem_st16(colS + c0 / 2, packed);
       }
+      tc::tmem_st16(colS, packed);
     };
     // dS^T over dP^T
     auto grads = [&](auto masked) {
       constexpr bool MASK = decltype(masked)::value;
       const RowStats& st = stats[g & 1];
+      uint32_t dp[32], packed[16];
+      tc::tmem_ld32(colP, dp);
+      tc::tmem_ld_wait();
 #pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t dp[32], packed[16];
-        tc::tmem_ld32(colP + c0, dp);
-        tc::tmem_ld_wait();
-        const uint32_t bits = (uint32_t)(see >> c0);
+      for (int c = 0; c < 32; c += 4) {
+        const ulonglong2 d4 = *reinterpret_cast<const ulonglong2*>(&st.ndelta[col0 + c]);
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const ulonglong2 d4 = *reinterpret_cast<const ulonglong2*>(&st.ndelta[half * 64 + c0 + c]);
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            float d0, d1;
-            f2_split(fmul2(pw[(c0 + c + e) / 2], fadd2(f2(__uint_as_float(dp[c + e]), __uint_as_float(dp[c + e + 1])),
-                                                       e == 0 ? d4.x : d4.y)), d0, d1);
-            if (MASK) {                       // dP of a hidden pair may be anything
-              d0 = (bits >> (c + e)) & 1u ? d0 : 0.f;
-              d1 = (bits >> (c + e + 1)) & 1u ? d1 : 0.f;
-            }
-            packed[(c + e) / 2] = pack_bf16(d0, d1);
+        for (int e = 0; e < 4; e += 2) {
+          float d0, d1;
+          f2_split(fmul2(pw[(c + e) / 2], fadd2(f2(__uint_as_float(dp[c + e]), __uint_as_float(dp[c + e + 1])),
+                                                e == 0 ? d4.x : d4.y)), d0, d1);
+          if (MASK) {                       // dP of a hidden pair may be anything
+            d0 = (see >> (c + e)) & 1u ? d0 : 0.f;
+            d1 = (see >> (c + e + 1)) & 1u ? d1 : 0.f;
           }
+          packed[(c + e) / 2] = pack_bf16(d0, d1);
         }
-        tc::tmem_st16(colP + c0 / 2, packed);
       }
+      tc::tmem_st16(colP, packed);
     };
 
+    const int jend = min(kT, seq.kv - j0);
+    const int2* tile_docs = doc_q != nullptr ? a.doc_blocks_q + (int64_t)b * tiles : nullptr;
+    const bool one_doc = bars->doc_lo == bars->doc_hi && !bars->doc_pad;
     bool ok = true;
-    for (; g < n; ++g) {
+    int t = walk.next(lane);
+    if (t >= 0) fetch(t);
+    for (; t >= 0; ++g) {
       const RowStats& st = stats[g & 1];
-      if (!warp_wait(&bars->q_full[g & 1], (g >> 1) & 1, abort) || !warp_wait(&bars->s_full, g & 1, abort)) {
-        fail(&bars->abort, 10);
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();
-      see = low64(bars->rows[g & 1] - half * 64);
-      const int masks = bars->masks[g & 1];
-      if (masks & 1) {
-        uint64_t below = 0ull;
+      const int i0 = t * qpt;
+      put(stats[g & 1]);
+      named_sync(1, kWork * 32);              // after an abort too: every warp takes all its turns
+      const int next = walk.next(lane);
+      if (next >= 0) fetch(next);
+      see = (uint32_t)(low64(min(qpt, a.Sq - i0) * a.G - col0) & 0xffffffffull);
+      // limits never fall along the rows: the first query's is the least
+      if (dense_limit(seq, a.causal, i0) - j0 < jend) {
+        uint32_t below = 0u;
 #pragma unroll 4
-        for (int c = 0; c < 64; c += 4) {
-          const int4 l = *reinterpret_cast<const int4*>(&st.limit[half * 64 + c]);
-          below |= (uint64_t)((r < l.x) | (r < l.y) << 1 | (r < l.z) << 2 | (r < l.w) << 3) << c;
+        for (int c = 0; c < 32; c += 4) {
+          const int4 l = *reinterpret_cast<const int4*>(&st.limit[col0 + c]);
+          below |= (uint32_t)((r < l.x) | (r < l.y) << 1 | (r < l.z) << 2 | (r < l.w) << 3) << c;
         }
         see &= below;
       }
-      if (masks & 2) {
-        see &= same_document(st.doc[half * 64 + lane], st.doc[half * 64 + 32 + lane], my_doc);
-        if (!key_ok) see = 0ull;
+      if (tile_docs != nullptr) {
+        const int2 v = tile_docs[t];
+        if (!one_doc || !doc_uniform(v) || v.y != bars->doc_lo) {
+          see &= (uint32_t)same_document(st.doc[col0 + lane], -1, my_doc);
+          if (!key_ok) see = 0u;
+        }
       }
-      const bool hidden = __any_sync(0xffffffffu, see != ~0ull);
-      if (hidden) probs(std::true_type{}); else probs(std::false_type{});
-      tc::tmem_st_wait();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->p_full);
-      if (!warp_wait(&bars->dp_full, g & 1, abort)) {
-        fail(&bars->abort, 11);
+      const bool hidden = __any_sync(0xffffffffu, see != 0xffffffffu);
+      if (ok && !warp_wait(&bars->s_full, g & 1, abort)) {
+        fail(&bars->abort, 10);
         ok = false;
-        break;
       }
-      tc::fence_after_sync();
-      if (hidden) grads(std::true_type{}); else grads(std::false_type{});
-      tc::tmem_st_wait();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+      if (ok) {
+        tc::fence_after_sync();
+        if (hidden) probs(std::true_type{}); else probs(std::false_type{});
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->p_full);
+        if (!warp_wait(&bars->dp_full, g & 1, abort)) {
+          fail(&bars->abort, 11);
+          ok = false;
+        }
+      }
+      if (ok) {
+        tc::fence_after_sync();
+        if (hidden) grads(std::true_type{}); else grads(std::false_type{});
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+      }
+      t = next;
     }
-    // ------------------------------------------------------------ results: one half writes dV, the other dK
+    // ------------------------------------------------------------ results: half the warps write dV, half dK
     if (n > 0 && ok) {
       if (!warp_wait(&bars->drain, 0, abort)) fail(&bars->abort, 12);
       tc::fence_after_sync();
     }
     const bool broken = __any_sync(0xffffffffu, *abort != 0);
-    const float by = broken ? __int_as_float(0x7fffffff) : half == 0 ? 1.f : a.scale;
-    const fvattn_strides& ss = half == 0 ? a.dvs : a.dks;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(half == 0 ? a.dv : a.dk) + (int64_t)b * ss.b + (int64_t)h * ss.h +
+    const int which = (warp - 2) >> 3, part_d = ((warp - 2) >> 2) & 1;
+    const float by = broken ? __int_as_float(0x7fffffff) : which == 0 ? 1.f : a.scale;
+    const fvattn_strides& ss = which == 0 ? a.dvs : a.dks;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which == 0 ? a.dv : a.dk) + (int64_t)b * ss.b + (int64_t)h * ss.h +
                          (int64_t)j * ss.s;
 #pragma unroll 1
-    for (int cc = 0; cc < D / 32; ++cc) {
+    for (int cc = part_d * (D / 64); cc < (part_d + 1) * (D / 64); ++cc) {
       uint32_t o[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] = 0u;
       if (n > 0 && !broken) {
-        tc::tmem_ld32(tbase + lanes + (half == 0 ? L::kColV : L::kColK) + cc * 32, o);
+        tc::tmem_ld32(tbase + lanes + (which == 0 ? L::kColV : L::kColK) + cc * 32, o);
         tc::tmem_ld_wait();
       }
       if (!key_ok && !broken) {
@@ -543,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars->s_full[s], 1);
     }
     tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->ds_full, kWork);
     tc::mbar_init(&bars->drain, 1);
     bars->abort = 0;
     bars->doc_lo = 0x7fffffff;
@@ -672,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ elementwise
-    const int q = warp & 3, half = (warp - 2) >> 2;      // TMEM lane quarter; first or second 64 keys of a tile
+    const int q = warp & 3, cg = (warp - 2) >> 2, col0 = cg * kCols;      // TMEM lane quarter, keys of a tile
     const int r = q * 32 + lane, i = i0 + r / a.G, hq = h * a.G + r % a.G;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const bool valid = r < qpt * a.G && i < a.Sq;
@@ -686,77 +695,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const ScoreMap<CAP, BIAS> map(a, row);
     const uint64_t after2 = f2(map.after, map.after), nlse2 = f2(-lse2, -lse2), ndelta2 = f2(-delta, -delta);
-    uint64_t pw[32];       // P, then P times the cap's derivative, in pairs
-    uint64_t see = ~0ull;  // bit c: this lane's row sees key c of this half
+    uint64_t pw[kCols / 2];          // P, then P times the cap's derivative, in pairs
+    uint32_t see = 0xffffffffu;      // bit c: this lane's row sees key c of this warp's
     uint32_t g = 0;
-    const uint32_t colP = tbase + lanes + L::kColDp + half * 64;
+    const uint32_t colP = tbase + lanes + L::kColDp + col0;
 
     auto probs = [&](auto masked, uint32_t colS, int far) {
       constexpr bool MASK = decltype(masked)::value;
+      uint32_t s[32];
+      tc::tmem_ld32(colS, s);
+      tc::tmem_ld_wait();
+      if (CAP) {
+        tanh32(s, map.in);
+        if (BIAS) {                         // kept for the derivative: the bias takes its place
 #pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t s[32];
-        tc::tmem_ld32(colS + c0, s);
-        tc::tmem_ld_wait();
-        if (CAP) {
-          tanh32(s, map.in);
-          if (BIAS) {                         // the derivative's factor, before the bias takes t's place
-#pragma unroll
-            for (int c = 0; c < 32; c += 2)
-              pw[(c0 + c) / 2] = f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          }
+          for (int c = 0; c < 32; c += 2) pw[c / 2] = f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         }
-        if (BIAS) map.bias(s, far - c0);
-        const uint32_t bits = (uint32_t)(see >> c0);
+      }
+      if (BIAS) map.bias(s, far);
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const uint64_t t2 = f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          float y0, y1;
-          f2_split(ffma2(t2, after2, nlse2), y0, y1);
-          float p0 = ex2(y0), p1 = ex2(y1);
-          if (MASK) {
-            p0 = (bits >> c) & 1u ? p0 : 0.f;
-            p1 = (bits >> (c + 1)) & 1u ? p1 : 0.f;
-          }
-          pw[(c0 + c) / 2] = CAP ? times_dcap(f2(p0, p1), BIAS ? pw[(c0 + c) / 2] : t2) : f2(p0, p1);
+      for (int c = 0; c < 32; c += 2) {
+        const uint64_t t2 = f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        float y0, y1;
+        f2_split(ffma2(t2, after2, nlse2), y0, y1);
+        float p0 = ex2(y0), p1 = ex2(y1);
+        if (MASK) {
+          p0 = (see >> c) & 1u ? p0 : 0.f;
+          p1 = (see >> (c + 1)) & 1u ? p1 : 0.f;
         }
+        pw[c / 2] = CAP ? times_dcap(f2(p0, p1), BIAS ? pw[c / 2] : t2) : f2(p0, p1);
       }
     };
-    // dS over the scores of this half, which are in registers
+    // dS over the scores of this warp, which are in registers
     auto grads = [&](auto masked, uint32_t colS) {
       constexpr bool MASK = decltype(masked)::value;
+      uint32_t dp[32], packed[16];
+      tc::tmem_ld32(colP, dp);
+      tc::tmem_ld_wait();
 #pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t dp[32], packed[16];
-        tc::tmem_ld32(colP + c0, dp);
-        tc::tmem_ld_wait();
-        const uint32_t bits = (uint32_t)(see >> c0);
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          float d0, d1;
-          f2_split(fmul2(pw[(c0 + c) / 2], fadd2(f2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), ndelta2)), d0, d1);
-          if (MASK) {                         // dP of a hidden pair may be anything
-            d0 = (bits >> c) & 1u ? d0 : 0.f;
-            d1 = (bits >> (c + 1)) & 1u ? d1 : 0.f;
-          }
-          packed[c / 2] = pack_bf16(d0, d1);
+      for (int c = 0; c < 32; c += 2) {
+        float d0, d1;
+        f2_split(fmul2(pw[c / 2], fadd2(f2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), ndelta2)), d0, d1);
+        if (MASK) {                         // dP of a hidden pair may be anything
+          d0 = (see >> c) & 1u ? d0 : 0.f;
+          d1 = (see >> (c + 1)) & 1u ? d1 : 0.f;
         }
-        tc::tmem_st16(colS + c0 / 2, packed);
+        packed[c / 2] = pack_bf16(d0, d1);
       }
+      tc::tmem_st16(colS, packed);
     };
 
     bool ok = true;
     for (int j; (j = walk.next(lane)) >= 0; ++g) {
-      const uint32_t colS = tbase + lanes + (g & 1 ? kColB : kColA) + half * 64;
-      const int first = j * kT + half * 64;
+      const uint32_t colS = tbase + lanes + (g & 1 ? kColB : kColA) + col0;
+      const int first = j * kT + col0;
+      see = (uint32_t)visible64(row, doc_k, doc_k != nullptr ? walk.docs[j] : make_int2(0, 0), first, a.Sk, lane);
+      const bool hidden = __any_sync(0xffffffffu, see != 0xffffffffu);
       if (!warp_wait(&bars->s_full[g & 1], (g >> 1) & 1, abort)) {
         fail(&bars->abort, 10);
         ok = false;
         break;
       }
       tc::fence_after_sync();
-      see = visible64(row, doc_k, doc_k != nullptr ? walk.docs[j] : make_int2(0, 0), first, a.Sk, lane);
-      const bool hidden = __any_sync(0xffffffffu, see != ~0ull);
       if (hidden) probs(std::true_type{}, colS, row.pos - first); else probs(std::false_type{}, colS, row.pos - first);
       if (!warp_wait(&bars->dp_full, g & 1, abort)) {
         fail(&bars->abort, 11);
@@ -778,9 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float by = broken ? __int_as_float(0x7fffffff) : a.scale;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + (int64_t)b * a.dqs.b + (int64_t)hq * a.dqs.h +
                          (int64_t)i * a.dqs.s;
-    // each half writes its half of the dims
+    // each column group of warps writes 32 dims
 #pragma unroll 1
-    for (int cc = half * (D / 64); cc < (half + 1) * (D / 64); ++cc) {
+    for (int cc = cg; cc < D / 32; cc += kWork / 4) {
       uint32_t o[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] = 0u;

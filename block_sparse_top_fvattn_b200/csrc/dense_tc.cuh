@@ -22,6 +22,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xffffffffu, ok);
 }
 
+// A barrier among `threads` threads of the CTA (id 0 is __syncthreads').
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // 2^x by the ex2.approx instruction (2^-inf = 0), and 1/x by rcp.approx (1/inf = 0).
 __device__ __forceinline__ float ex2(float x) {
   float y;
