@@ -70,7 +70,7 @@ int validate_dense(const fvattn_dense_shape* s, const fvattn_dense_mask* m, bool
   if (s->causal != 0 && s->causal != 1) return FVATTN_ERR_INVALID;
   if (s->Hq % s->Hkv != 0) return FVATTN_ERR_INVALID;
   if (s->d != 64 && s->d != 128) return FVATTN_ERR_UNSUPPORTED;
-  if (s->Hq / s->Hkv > 128 || s->B > 65535 || s->Hkv > 65535) return FVATTN_ERR_UNSUPPORTED;
+  if (s->Hq / s->Hkv > 64 || s->B > 65535 || s->Hkv > 65535) return FVATTN_ERR_UNSUPPORTED;
   if (s->Sq > kPosMax || s->Sk > kPosMax || s->Sq * (s->Hq / s->Hkv) > (int64_t)1 << 34) return FVATTN_ERR_UNSUPPORTED;
   if (!valid_strides(s->q, s->B, s->Hq, s->Sq, s->dtype) || !valid_strides(s->k, s->B, s->Hkv, s->Sk, s->dtype) ||
       !valid_strides(s->v, s->B, s->Hkv, s->Sk, s->dtype) || !valid_strides(s->o, s->B, s->Hq, s->Sq, s->dtype))
@@ -157,14 +157,14 @@ DenseWs fwd_ws(const DenseArgs& a, int dtype) {
   return w;
 }
 
-constexpr int kBwdKeys = 128;      // keys of a tile of the gradients' kernels
+constexpr int kBwdKeys = 128, kBwdRows = 64;      // of a tile of dQ's keys, and of dK and dV's rows
 
 DenseWs bwd_ws(const DenseArgs& a, int dtype) {
   DenseWs w{};
   size_t off = 0;
   w.delta = take(off, (size_t)a.B * a.Hq * a.Sq * sizeof(float));
   if (dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
-    w.docs_q = take(off, doc_bytes(a.B, a.Sq, kTileRows / a.G));
+    w.docs_q = take(off, doc_bytes(a.B, a.Sq, kBwdRows / a.G));
     w.docs_k = take(off, doc_bytes(a.B, a.Sk, kBwdKeys));
   }
   w.total = off;
@@ -324,7 +324,7 @@ int fvattn_dense_attn_bwd(const void* dout, const void* q, const void* k, const 
   if (e == cudaSuccess && shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
     a.doc_blocks_q = reinterpret_cast<int2*>(ws + w.docs_q);
     a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
-    e = launch_dense_docs(a.mask.doc_q, a.doc_blocks_q, a.B, a.Sq, kTileRows / a.G, s);
+    e = launch_dense_docs(a.mask.doc_q, a.doc_blocks_q, a.B, a.Sq, kBwdRows / a.G, s);
     if (e == cudaSuccess) e = launch_dense_docs(a.mask.doc_k, a.doc_blocks_k, a.B, a.Sk, kBwdKeys, s);
   }
   if (e == cudaSuccess) e = shape->dtype == FVATTN_BF16 ? launch_dense_bwd_tc(a, s) : launch_dense_f32_bwd(a, s);

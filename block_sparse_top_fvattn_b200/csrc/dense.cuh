@@ -30,7 +30,7 @@ struct DenseArgs {
   float *part_o, *part_lse;       // splits > 1: [splits][B][Hq][Sq][d] and [splits][B][Hq][Sq]
   float* delta;                   // backward: [B][Hq][Sq], sum_d out * dout
   // Documents of blocks of tokens (dense_doc_kernel), null without documents: of the keys in blocks of
-  // 64 (forward) or 128 (backward), of the queries in row tiles (backward).
+  // 64 (forward) or 128 (backward), of the queries in steps of dK and dV (backward).
   int2 *doc_blocks_q, *doc_blocks_k;
   int32_t* status;
 };

@@ -10,9 +10,11 @@
 // gradient is summed over its query heads in TMEM.
 //
 // dK, dV: scores transposed (lane = key, column = row), so that P^T and dS^T are written over the
-// scores in TMEM as the first operands of their products. Per tile, with sixteen warps between them:
-//   products   dV(i) S(i+1)            | dK(i) dP(i+1)
-//   warps      dS(i) from dP(i), P(i)  | P(i+1) from S(i+1)
+// scores in TMEM as the first operands of their products. Steps of 64 rows alternate between two groups
+// of eight warps, each with its own scores and dP in TMEM, so that one group's exponentials run beside
+// the other's and beside the products of both:
+//   products of slot k    dV(k) S(k+2) dK(k-1) dP(k+1)
+//   one group             P(k) from S(k), in slot k-1;      dS(k) from dP(k), in slot k
 // dQ: lane = row; S has two buffers, so S(i+1) is ready when dS(i) is done:
 //   products   dP(i+1) dQ(i) S(i+2);   warps   P(i+1), then dS(i+1) from dP(i+1)
 //
@@ -50,30 +52,30 @@ struct BwdLayout {
   static constexpr int kTile = (D / 64) * kChunk;
 };
 
-// A token-by-dims tile as the K-major operand of a product over dims, and as the MN-major second operand
-// of a product over tokens.
-__device__ __forceinline__ uint64_t desc_dims(uint32_t addr, int kk) {
-  return tc::smem_desc_sw128(addr + (kk >> 2) * (kT * 128) + (kk & 3) * 32, 16, 1024);
-}
-__device__ __forceinline__ uint64_t desc_tokens(uint32_t addr, int kk) {
-  return tc::smem_desc_sw128(addr + kk * 16 * 128, kT * 128, 1024);
-}
+// Shared-memory descriptors of a token-by-dims tile: as the K-major operand of a product over dims, and
+// as the MN-major second operand of a product over tokens. Within a tile only the address field (the
+// low bits, in units of 16 bytes) changes, so a step costs the issuing thread one addition.
+__device__ __forceinline__ uint64_t desc_dims(uint32_t addr) { return tc::smem_desc_sw128(addr, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_tokens(uint32_t addr) { return tc::smem_desc_sw128(addr, kT * 128, 1024); }
+constexpr uint32_t step_dims(int kk) { return ((kk >> 2) * (kT * 128) + (kk & 3) * 32) >> 4; }
+constexpr uint32_t step_tokens(int kk) { return (kk * 16 * 128) >> 4; }
 
 // D[128 x 128] = A B^T over the dims of two tiles.
 template <int D>
-__device__ __forceinline__ void mma_dims(uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr) {
+__device__ __forceinline__ void mma_dims(uint32_t d_tmem, uint64_t a, uint64_t b) {
   constexpr uint32_t id = tc::idesc_bf16_f32(kT, kT, 0, 0);
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) tc::mma_f16(d_tmem, desc_dims(a_addr, kk), desc_dims(b_addr, kk), id, kk > 0);
+  for (int kk = 0; kk < D / 16; ++kk) tc::mma_f16(d_tmem, a + step_dims(kk), b + step_dims(kk), id, kk > 0);
 }
 // D[128 x D] (+)= W B over the 128 tokens of a tile, W (bf16) in TMEM: every kCols tokens over the fp32
 // values they were made from.
 template <int D>
-__device__ __forceinline__ void mma_tokens(uint32_t d_tmem, uint32_t w, uint32_t b_addr, bool add) {
+__device__ __forceinline__ void mma_tokens(uint32_t d_tmem, uint32_t w, uint64_t b, uint32_t add) {
   constexpr uint32_t id = tc::idesc_bf16_f32(kT, D, 0, 1);
 #pragma unroll
   for (int kk = 0; kk < kT / 16; ++kk)
-    tc::mma_f16_tmem_a(d_tmem, w + (kk / (kCols / 16)) * kCols + (kk % (kCols / 16)) * 8, desc_tokens(b_addr, kk), id, add || kk > 0);
+    tc::mma_f16_tmem_a(d_tmem, w + (kk / (kCols / 16)) * kCols + (kk % (kCols / 16)) * 8, b + step_tokens(kk), id,
+                       kk > 0 ? 1u : add);
 }
 
 // 32 fp32 results, times `by`, as bf16.
@@ -85,31 +87,37 @@ __device__ __forceinline__ void store32(__nv_bfloat16* p, uint32_t (&o)[32], flo
 
 // ------------------------------------------------------------------ dK, dV
 
-// What a row tile's rows need, per stage.
+constexpr int kR = 64;                // rows of a step
+constexpr int kStagesQ = 5;           // S(k+2) is issued before dK(k-1) has released Q(k-1)
+constexpr int kStagesG = 4;
+
+// What the rows of a step need, twice per group.
 struct RowStats {
-  float nlse2[kT];     // - lse log2 e
-  float ndelta[kT];    // - delta
-  float far[kT];       // position minus the first key of the key tile
-  float slope2[kT];    // slope log2 e
-  int limit[kT];       // visible keys are below it, counted from the first key of the key tile
-  int doc[kT];
+  float nlse2[kR];     // - lse log2 e
+  float ndelta[kR];    // - delta
+  float far[kR];       // position minus the first key of the key tile
+  float slope2[kR];    // slope log2 e
+  int limit[kR];       // visible keys are below it, counted from the first key of the key tile
+  int doc[kR];
 };
 
 template <int D>
-struct DkvLayout : BwdLayout<D> {
-  using B = BwdLayout<D>;
-  static constexpr int kOffK = 0, kOffV = B::kTile, kOffQ = 2 * B::kTile, kOffG = 4 * B::kTile;
-  static constexpr int kOffStats = 6 * B::kTile;
-  static constexpr int kOffBar = kOffStats + 2 * (int)sizeof(RowStats);
-  static constexpr int kBytes = kOffBar + 256;
-  static constexpr uint32_t kColV = 256, kColK = 384;
+struct DkvLayout {
+  static constexpr int kKeyChunk = kT * 128, kKeyTile = (D / 64) * kKeyChunk;    // [tokens x 64 dims] bf16
+  static constexpr int kRowChunk = kR * 128, kRowTile = (D / 64) * kRowChunk;
+  static constexpr int kOffK = 0, kOffV = kKeyTile, kOffQ = 2 * kKeyTile, kOffG = kOffQ + kStagesQ * kRowTile;
+  static constexpr int kOffStats = kOffG + kStagesG * kRowTile;
+  static constexpr int kOffBar = kOffStats + 4 * (int)sizeof(RowStats);
+  static constexpr int kBytes = kOffBar + 512;
+  // TMEM: scores of even and odd steps, dP of even and odd steps, the results
+  static constexpr uint32_t kColS = 0, kColDp = 128, kColV = 256, kColK = 384;
 };
 
 struct DkvBars {
   uint64_t kv_full;
-  uint64_t q_full[2], q_empty[2];     // Q of a tile
-  uint64_t g_full[2], g_empty[2];     // dout of a tile
-  uint64_t s_full, p_full, dp_full, ds_full;
+  uint64_t q_full[kStagesQ], q_empty[kStagesQ];
+  uint64_t g_full[kStagesG], g_empty[kStagesG];      // dout
+  uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2];
   uint64_t drain;
   int doc_lo, doc_hi, doc_pad;        // documents of the keys
   uint32_t tmem_base;
@@ -120,14 +128,12 @@ template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const DenseArgs a, const int qpt,
-                       const TileOrder order) {
+                        const DenseArgs a, const int qpt, const TileOrder order) {
   using L = DkvLayout<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   DkvBars* bars = reinterpret_cast<DkvBars*>(smem + L::kOffBar);
-  RowStats* stats = reinterpret_cast<RowStats*>(smem + L::kOffStats);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
   int x, bh;
@@ -140,16 +146,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->kv_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kStagesQ; ++s) {
       tc::mbar_init(&bars->q_full[s], 1);
       tc::mbar_init(&bars->q_empty[s], 1);
+    }
+    for (int s = 0; s < kStagesG; ++s) {
       tc::mbar_init(&bars->g_full[s], 1);
       tc::mbar_init(&bars->g_empty[s], 1);
     }
-    tc::mbar_init(&bars->s_full, 1);
-    tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->p_full, kWork);
-    tc::mbar_init(&bars->ds_full, kWork);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&bars->s_full[s], 1);
+      tc::mbar_init(&bars->dp_full[s], 1);
+      tc::mbar_init(&bars->p_full[s], kWork / 2);
+      tc::mbar_init(&bars->ds_full[s], kWork / 2);
+    }
     tc::mbar_init(&bars->drain, 1);
     bars->abort = 0;
     bars->doc_lo = 0x7fffffff;
@@ -161,10 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(&bars->tmem_base, 512);
     tc::tmem_relinquish();
   }
-  // Rows that no copy writes (128 - qpt * G of them) have weights of zero: they must hold numbers.
-  if (qpt * a.G < kT) {
-    for (int x = threadIdx.x; x < 4 * L::kTile / 16; x += kThreads)
-      reinterpret_cast<uint4*>(smem + L::kOffQ)[x] = make_uint4(0u, 0u, 0u, 0u);
+  // Rows that no copy writes (64 - qpt * G of them) have weights of zero: they must hold numbers.
+  if (qpt * a.G < kR) {
+    for (int i = threadIdx.x; i < (kStagesQ + kStagesG) * L::kRowTile / 16; i += kThreads)
+      reinterpret_cast<uint4*>(smem + L::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_proxy_async_smem();
   }
   tc::fence_before_sync();
@@ -182,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  const uint32_t tbase = bars->tmem_base;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   // Under an order the rows from the first whose limit passes j0 see the tile (limits never fall).
   int first = 0;
   if (j0 >= seq.kv) {
@@ -190,166 +200,196 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (a.causal && j0 >= seq.prefix) {
     first = max(0, min(j0 - seq.q0, a.Sq)) / qpt;      // query i sees key j0 when q0 + i >= j0
   }
-  BlockWalk walk(a.doc_blocks_q != nullptr ? a.doc_blocks_q + (int64_t)b * tiles : nullptr, first, tiles, bars->doc_lo,
-                bars->doc_hi);
+  const int2* tile_docs = doc_q != nullptr ? a.doc_blocks_q + (int64_t)b * tiles : nullptr;
+  BlockWalk walk(tile_docs, first, tiles, bars->doc_lo, bars->doc_hi);
   const uint32_t n = (uint32_t)walk.count(lane);
 
   if (warp == 0) {
     // ------------------------------------------------------------ loader
     bool kv_armed = false;
-    int q_par[2] = {-1, -1}, g_par[2] = {-1, -1};
     if (lane == 0 && n > 0) {
-      tc::mbar_expect_tx(&bars->kv_full, 2 * L::kTile);
+      tc::mbar_expect_tx(&bars->kv_full, 2 * L::kKeyTile);
       kv_armed = true;
       for (int c = 0; c < D / 64; ++c) {
-        tc::tma_load_4d(smem + L::kOffK + c * L::kChunk, &tmK, &bars->kv_full, c * 64, j0, h, b);
-        tc::tma_load_4d(smem + L::kOffV + c * L::kChunk, &tmV, &bars->kv_full, c * 64, j0, h, b);
+        tc::tma_load_4d(smem + L::kOffK + c * L::kKeyChunk, &tmK, &bars->kv_full, c * 64, j0, h, b);
+        tc::tma_load_4d(smem + L::kOffV + c * L::kKeyChunk, &tmV, &bars->kv_full, c * 64, j0, h, b);
       }
     }
     const uint32_t bytes = (uint32_t)(qpt * a.G) * 128 * (D / 64);
-    uint32_t g = 0;
+    uint32_t g = 0, q_armed = 0, g_armed = 0;      // steps whose copies were issued
     for (int t; (t = walk.next(lane)) >= 0; ++g) {
-      const int s = g & 1;
-      const uint32_t par = (g >> 1) & 1;
-      const int i0 = t * qpt;
+      const int sq = g % kStagesQ, sg = g % kStagesG, i0 = t * qpt;
       // padding queries may hold anything: their tiles are copied by hand, with zeros for them
-      const bool pad = doc_q != nullptr && a.doc_blocks_q[(int64_t)b * tiles + t].x < 0;
-      unsigned char *sq = smem + L::kOffQ + s * L::kTile, *sg = smem + L::kOffG + s * L::kTile;
-      if (!warp_wait(&bars->q_empty[s], par ^ 1, abort)) {
+      const bool pad = tile_docs != nullptr && tile_docs[t].x < 0;
+      unsigned char *dq = smem + L::kOffQ + sq * L::kRowTile, *dg = smem + L::kOffG + sg * L::kRowTile;
+      if (!warp_wait(&bars->q_empty[sq], ((g / kStagesQ) & 1) ^ 1, abort)) {
         fail(&bars->abort, 3);
         break;
       }
-      if (!pad) {
-        if (lane == 0) {
-          tc::mbar_expect_tx(&bars->q_full[s], bytes);
-          for (int c = 0; c < D / 64; ++c)
-            tc::tma_load_5d(sq + c * L::kChunk, &tmQ, &bars->q_full[s], c * 64, 0, i0, h, b);
-        }
-      } else {
-        copy_rows<D>(sq, static_cast<const __nv_bfloat16*>(a.q), a.qs, a, b, h, i0, qpt, doc_q, lane, 32);
+      if (pad) {
+        copy_rows<D, kR>(dq, static_cast<const __nv_bfloat16*>(a.q), a.qs, a, b, h, i0, qpt, doc_q, lane, 32);
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->q_full[s]);
+        if (lane == 0) tc::mbar_arrive(&bars->q_full[sq]);
+      } else if (lane == 0) {
+        tc::mbar_expect_tx(&bars->q_full[sq], bytes);
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_5d(dq + c * L::kRowChunk, &tmQ, &bars->q_full[sq], c * 64, 0, i0, h, b);
       }
-      q_par[s] = (int)par;
-      if (!warp_wait(&bars->g_empty[s], par ^ 1, abort)) {
+      q_armed = g + 1;
+      if (!warp_wait(&bars->g_empty[sg], ((g / kStagesG) & 1) ^ 1, abort)) {
         fail(&bars->abort, 4);
         break;
       }
-      if (!pad) {
-        if (lane == 0) {
-          tc::mbar_expect_tx(&bars->g_full[s], bytes);
-          for (int c = 0; c < D / 64; ++c)
-            tc::tma_load_5d(sg + c * L::kChunk, &tmG, &bars->g_full[s], c * 64, 0, i0, h, b);
-        }
-      } else {
-        copy_rows<D>(sg, static_cast<const __nv_bfloat16*>(a.dout), a.dos, a, b, h, i0, qpt, doc_q, lane, 32);
+      if (pad) {
+        copy_rows<D, kR>(dg, static_cast<const __nv_bfloat16*>(a.dout), a.dos, a, b, h, i0, qpt, doc_q, lane, 32);
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->g_full[s]);
+        if (lane == 0) tc::mbar_arrive(&bars->g_full[sg]);
+      } else if (lane == 0) {
+        tc::mbar_expect_tx(&bars->g_full[sg], bytes);
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_5d(dg + c * L::kRowChunk, &tmG, &bars->g_full[sg], c * 64, 0, i0, h, b);
       }
-      g_par[s] = (int)par;
+      g_armed = g + 1;
     }
     if (lane == 0) {
-      // no copy may still be writing shared memory when the CTA leaves
+      // no copy may still be writing shared memory when the CTA leaves: the last of each stage
       if (kv_armed) tc::mbar_wait_drain(&bars->kv_full, 0, kWaitLimit);
-      for (int s = 0; s < 2; ++s) {
-        if (q_par[s] >= 0) tc::mbar_wait_drain(&bars->q_full[s], (uint32_t)q_par[s], kWaitLimit);
-        if (g_par[s] >= 0) tc::mbar_wait_drain(&bars->g_full[s], (uint32_t)g_par[s], kWaitLimit);
-      }
+      for (uint32_t k = q_armed > kStagesQ ? q_armed - kStagesQ : 0; k < q_armed; ++k)
+        tc::mbar_wait_drain(&bars->q_full[k % kStagesQ], (k / kStagesQ) & 1, kWaitLimit);
+      for (uint32_t k = g_armed > kStagesG ? g_armed - kStagesG : 0; k < g_armed; ++k)
+        tc::mbar_wait_drain(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, kWaitLimit);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n > 0) {
-      const uint32_t ka = tc::smem_u32(smem + L::kOffK), va = tc::smem_u32(smem + L::kOffV);
-      const uint32_t qa = tc::smem_u32(smem + L::kOffQ), ga = tc::smem_u32(smem + L::kOffG);
+    // The whole warp keeps step, so that what the products take is the same in all lanes; one lane issues.
+    if (n > 0) {
+      constexpr uint32_t idS = tc::idesc_bf16_f32(kT, kR, 0, 0), idD = tc::idesc_bf16_f32(kT, D, 0, 1);
+      const uint64_t ka = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffK), 16, 1024);
+      const uint64_t va = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffV), 16, 1024);
+      const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffQ), 16, 1024);
+      const uint64_t gd = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffG), 16, 1024);
+      const uint64_t qt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffQ), L::kRowChunk, 1024);
+      const uint64_t gt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffG), L::kRowChunk, 1024);
+      constexpr uint32_t kStage = L::kRowTile >> 4;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
-        if (ok && !tc::mbar_wait(bar, parity, abort, kWaitLimit)) {
-          fail(&bars->abort, code);
-          ok = false;
-        }
+        ok = ok && warp_wait(bar, parity, abort);
+        if (!ok) fail(&bars->abort, code);
         tc::fence_after_sync();
         return ok;
       };
-      auto scores = [&](uint32_t g) {
-        if (!wait(&bars->q_full[g & 1], (g >> 1) & 1, 5)) return;
-        mma_dims<D>(tbase + kColA, ka, qa + (g & 1) * L::kTile);
-        tc::mma_commit(&bars->s_full);
+      // scores^T or dP^T of a step: [128 keys x 64 rows] over the dims
+      auto over_dims = [&](uint32_t d_tmem, uint64_t key_tile, uint64_t row_tile, uint64_t* done) {
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_f16(d_tmem, key_tile + (((kk >> 2) * L::kKeyChunk + (kk & 3) * 32) >> 4),
+                        row_tile + (((kk >> 2) * L::kRowChunk + (kk & 3) * 32) >> 4), idS, kk > 0);
+          tc::mma_commit(done);
+        }
+        __syncwarp();
       };
-      auto dprobs = [&](uint32_t g) {
-        if (!wait(&bars->g_full[g & 1], (g >> 1) & 1, 6)) return;
-        mma_dims<D>(tbase + kColB, va, ga + (g & 1) * L::kTile);
-        tc::mma_commit(&bars->dp_full);
+      // dV or dK += [128 keys x 64 rows] (bf16 in TMEM, every kCols rows over their fp32 values) x [rows x D]
+      auto over_rows = [&](uint32_t d_tmem, uint32_t w, uint64_t row_tile, uint32_t add, uint64_t* done) {
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kR / 16; ++kk)
+            tc::mma_f16_tmem_a(d_tmem, w + (kk >> 1) * kCols + (kk & 1) * 8, row_tile + ((kk * 16 * 128) >> 4), idD,
+                               kk > 0 ? 1u : add);
+          tc::mma_commit(done);
+        }
+        __syncwarp();
+      };
+      auto scores = [&](uint32_t k) {
+        if (!wait(&bars->q_full[k % kStagesQ], (k / kStagesQ) & 1, 5)) return;
+        over_dims(tbase + L::kColS + (k & 1) * kR, ka, qd + (k % kStagesQ) * kStage, &bars->s_full[k & 1]);
+      };
+      auto dprobs = [&](uint32_t k) {
+        if (!wait(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, 6)) return;
+        over_dims(tbase + L::kColDp + (k & 1) * kR, va, gd + (k % kStagesG) * kStage, &bars->dp_full[k & 1]);
       };
       wait(&bars->kv_full, 0, 7);
       if (ok) scores(0);
       if (ok) dprobs(0);
-      for (uint32_t g = 0; ok && g < n; ++g) {
-        if (!wait(&bars->p_full, g & 1, 8)) break;
-        mma_tokens<D>(tbase + L::kColV, tbase + kColA, ga + (g & 1) * L::kTile, g > 0);
-        tc::mma_commit(&bars->g_empty[g & 1]);
-        if (g + 1 < n) scores(g + 1);
-        if (!wait(&bars->ds_full, g & 1, 9)) break;
-        mma_tokens<D>(tbase + L::kColK, tbase + kColB, qa + (g & 1) * L::kTile, g > 0);
-        tc::mma_commit(&bars->q_empty[g & 1]);
-        if (g + 1 < n) dprobs(g + 1);
+      if (ok && n > 1) scores(1);
+      for (uint32_t k = 0; ok && k <= n; ++k) {
+        if (k < n) {
+          if (!wait(&bars->p_full[k & 1], (k >> 1) & 1, 8)) break;
+          over_rows(tbase + L::kColV, tbase + L::kColS + (k & 1) * kR, gt + (k % kStagesG) * kStage, k > 0,
+                    &bars->g_empty[k % kStagesG]);
+          if (k + 2 < n) scores(k + 2);
+        }
+        if (k > 0) {
+          if (!wait(&bars->ds_full[(k - 1) & 1], ((k - 1) >> 1) & 1, 9)) break;
+          over_rows(tbase + L::kColK, tbase + L::kColDp + ((k - 1) & 1) * kR, qt + ((k - 1) % kStagesQ) * kStage, k > 1,
+                    &bars->q_empty[(k - 1) % kStagesQ]);
+        }
+        if (k + 1 < n) dprobs(k + 1);
       }
       // on every path: the products issued so far are done before TMEM is read or released
-      tc::mma_commit(&bars->drain);
-      tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+      if (tc::elect_one()) {
+        tc::mma_commit(&bars->drain);
+        tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ elementwise
-    const int q = warp & 3, col0 = ((warp - 2) >> 2) * kCols;      // TMEM lane quarter, rows of a tile
+    // TMEM lane quarter, group (steps of its parity), columns of the step
+    const int q = warp & 3, group = (warp - 2) >> 3, col0 = (((warp - 2) >> 2) & 1) * kCols;
     const int r = q * 32 + lane, j = j0 + r;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const uint32_t colS = tbase + lanes + kColA + col0, colP = tbase + lanes + kColB + col0;
+    const uint32_t colS = tbase + lanes + L::kColS + group * kR + col0, colP = tbase + lanes + L::kColDp + group * kR + col0;
+    RowStats* stats = reinterpret_cast<RowStats*>(smem + L::kOffStats) + 2 * group;
     const int my_doc = doc_k != nullptr && j < a.Sk ? doc_k[j] : 0;
     const bool key_ok = j < seq.kv && my_doc >= 0;
     const float in = CAP ? a.scale / a.cap : 0.f, factor = (CAP ? a.cap : a.scale) * kLog2e, fr = (float)r;
     const uint64_t factor2 = f2(factor, factor);
     uint64_t pw[kCols / 2];          // P, then P times the cap's derivative, in pairs
     uint32_t see = 0xffffffffu;      // bit c: row c of this warp's sees this lane's key
-    uint32_t g = 0;
 
-    // The row statistics of a tile: these threads hold one value each of the next tile's in flight, and
-    // write it at the start of its turn.
-    const int part = (threadIdx.x - 64) / kT, sr = (threadIdx.x - 64) % kT;
-    float ahead0 = 0.f, ahead1 = 0.f;
+    // The row statistics of a step: these threads hold one value each of the group's next step in flight,
+    // as loaded (nothing waits for it), and write it at the start of its turn.
+    const int tid = threadIdx.x - 64 - group * (kWork / 2) * 32;
+    const int part = tid / kR, sr = tid % kR, si = sr / a.G, sg = sr - si * a.G;
+    float ahead = 0.f;       // lse, delta, document or slope of row sr
+    int ahead_limit = 0;     // its limit or position
     auto fetch = [&](int t) {
-      const int i0 = t * qpt, i = i0 + sr / a.G, hq = h * a.G + sr % a.G;
-      const bool row_ok = sr < min(qpt, a.Sq - i0) * a.G;
+      const int i0 = t * qpt, i = i0 + si, hq = h * a.G + sg;
+      ahead = 0.f;
+      ahead_limit = 0;
+      if (sr >= min(qpt, a.Sq - i0) * a.G) return;
       const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + i;
-      if (part == 0) {
-        ahead0 = row_ok ? -a.lse[flat] * kLog2e : 0.f;
-      } else if (part == 1) {
-        ahead0 = row_ok ? -a.delta[flat] : 0.f;
-      } else {
-        DenseRow row{0, -1, 0, 0.f};
-        if (row_ok) row = dense_row(a, seq, b, hq, i);
-        ahead0 = part == 2 ? __int_as_float(row.limit - j0) : (float)(row.pos - j0);
-        ahead1 = part == 2 ? __int_as_float(row.doc) : row.slope * kLog2e;
+      if (part == 0) ahead = a.lse[flat];
+      if (part == 1) ahead = a.delta[flat];
+      if (part == 2) {
+        ahead_limit = dense_limit(seq, a.causal, i);
+        if (doc_q != nullptr) ahead = __int_as_float(doc_q[i]);
+      }
+      if (BIAS && part == 3) {
+        ahead_limit = seq.q0 + i;
+        ahead = a.mask.slopes[hq];
       }
     };
     auto put = [&](RowStats& st) {
-      if (part == 0) {
-        st.nlse2[sr] = ahead0;
-      } else if (part == 1) {
-        st.ndelta[sr] = ahead0;
-      } else if (part == 2) {
-        st.limit[sr] = __float_as_int(ahead0);
-        st.doc[sr] = __float_as_int(ahead1);
-      } else {
-        st.far[sr] = ahead0;
-        st.slope2[sr] = ahead1;
+      if (part == 0) st.nlse2[sr] = -ahead * kLog2e;
+      if (part == 1) st.ndelta[sr] = -ahead;
+      if (part == 2) {
+        const int doc = __float_as_int(ahead);
+        st.limit[sr] = (doc < 0 ? 0 : ahead_limit) - j0;
+        st.doc[sr] = doc;
+      }
+      if (BIAS && part == 3) {
+        st.far[sr] = (float)(ahead_limit - j0);
+        st.slope2[sr] = ahead * kLog2e;
       }
     };
 
     // P^T of this warp's rows over the scores it is made from, loaded by then
-    auto probs = [&](auto masked) {
+    auto probs = [&](auto masked, const RowStats& st) {
       constexpr bool MASK = decltype(masked)::value;
-      const RowStats& st = stats[g & 1];
       uint32_t s[32], packed[16];
       tc::tmem_ld32(colS, s);
       tc::tmem_ld_wait();
@@ -379,9 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_st16(colS, packed);
     };
     // dS^T over dP^T
-    auto grads = [&](auto masked) {
+    auto grads = [&](auto masked, const RowStats& st) {
       constexpr bool MASK = decltype(masked)::value;
-      const RowStats& st = stats[g & 1];
       uint32_t dp[32], packed[16];
       tc::tmem_ld32(colP, dp);
       tc::tmem_ld_wait();
@@ -404,16 +443,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     const int jend = min(kT, seq.kv - j0);
-    const int2* tile_docs = doc_q != nullptr ? a.doc_blocks_q + (int64_t)b * tiles : nullptr;
     const bool one_doc = bars->doc_lo == bars->doc_hi && !bars->doc_pad;
     bool ok = true;
     int t = walk.next(lane);
+    if (group == 1) t = walk.next(lane);
     if (t >= 0) fetch(t);
-    for (; t >= 0; ++g) {
-      const RowStats& st = stats[g & 1];
+    for (uint32_t turn = 0; t >= 0; ++turn) {
+      RowStats& st = stats[turn & 1];
       const int i0 = t * qpt;
-      put(stats[g & 1]);
-      named_sync(1, kWork * 32);              // after an abort too: every warp takes all its turns
+      put(st);
+      named_sync(1 + group, kWork / 2 * 32);      // after an abort too: every warp takes all its turns
+      walk.next(lane);                            // the other group's
       const int next = walk.next(lane);
       if (next >= 0) fetch(next);
       see = (uint32_t)(low64(min(qpt, a.Sq - i0) * a.G - col0) & 0xffffffffull);
@@ -435,42 +475,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const bool hidden = __any_sync(0xffffffffu, see != 0xffffffffu);
-      if (ok && !warp_wait(&bars->s_full, g & 1, abort)) {
+      if (ok && !warp_wait(&bars->s_full[group], turn & 1, abort)) {
         fail(&bars->abort, 10);
         ok = false;
       }
       if (ok) {
         tc::fence_after_sync();
-        if (hidden) probs(std::true_type{}); else probs(std::false_type{});
+        if (hidden) probs(std::true_type{}, st); else probs(std::false_type{}, st);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->p_full);
-        if (!warp_wait(&bars->dp_full, g & 1, abort)) {
+        if (lane == 0) tc::mbar_arrive(&bars->p_full[group]);
+        if (!warp_wait(&bars->dp_full[group], turn & 1, abort)) {
           fail(&bars->abort, 11);
           ok = false;
         }
       }
       if (ok) {
         tc::fence_after_sync();
-        if (hidden) grads(std::true_type{}); else grads(std::false_type{});
+        if (hidden) grads(std::true_type{}, st); else grads(std::false_type{}, st);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+        if (lane == 0) tc::mbar_arrive(&bars->ds_full[group]);
       }
       t = next;
     }
-    // ------------------------------------------------------------ results: half the warps write dV, half dK
+    // ------------------------------------------------------------ results: one group writes dV, the other dK
     if (n > 0 && ok) {
       if (!warp_wait(&bars->drain, 0, abort)) fail(&bars->abort, 12);
       tc::fence_after_sync();
     }
     const bool broken = __any_sync(0xffffffffu, *abort != 0);
-    const int which = (warp - 2) >> 3, part_d = ((warp - 2) >> 2) & 1;
-    const float by = broken ? __int_as_float(0x7fffffff) : which == 0 ? 1.f : a.scale;
-    const fvattn_strides& ss = which == 0 ? a.dvs : a.dks;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which == 0 ? a.dv : a.dk) + (int64_t)b * ss.b + (int64_t)h * ss.h +
+    const int part_d = ((warp - 2) >> 2) & 1;
+    const float by = broken ? __int_as_float(0x7fffffff) : group == 0 ? 1.f : a.scale;
+    const fvattn_strides& ss = group == 0 ? a.dvs : a.dks;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(group == 0 ? a.dv : a.dk) + (int64_t)b * ss.b + (int64_t)h * ss.h +
                          (int64_t)j * ss.s;
 #pragma unroll 1
     for (int cc = part_d * (D / 64); cc < (part_d + 1) * (D / 64); ++cc) {
@@ -478,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] = 0u;
       if (n > 0 && !broken) {
-        tc::tmem_ld32(tbase + lanes + (which == 0 ? L::kColV : L::kColK) + cc * 32, o);
+        tc::tmem_ld32(tbase + lanes + (group == 0 ? L::kColV : L::kColK) + cc * 32, o);
         tc::tmem_ld_wait();
       }
       if (!key_ok && !broken) {
@@ -576,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  const uint32_t tbase = bars->tmem_base;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   const int key1 = dense_limit(seq, a.causal, i1 - 1);
   BlockWalk walk(a.doc_blocks_k != nullptr ? a.doc_blocks_k + (int64_t)b * blocks : nullptr, 0, (key1 + kT - 1) / kT,
                  bars->doc_lo, bars->doc_hi);
@@ -642,28 +682,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n > 0) {
-      const uint32_t qa = tc::smem_u32(smem + L::kOffQ), ga = tc::smem_u32(smem + L::kOffG);
-      const uint32_t ka = tc::smem_u32(smem + L::kOffK), va = tc::smem_u32(smem + L::kOffV);
+    // The whole warp keeps step, so that what the products take is the same in all lanes; one lane issues.
+    if (n > 0) {
+      const uint64_t qa = desc_dims(tc::smem_u32(smem + L::kOffQ)), ga = desc_dims(tc::smem_u32(smem + L::kOffG));
+      const uint64_t kd = desc_dims(tc::smem_u32(smem + L::kOffK)), vd = desc_dims(tc::smem_u32(smem + L::kOffV));
+      const uint64_t kt = desc_tokens(tc::smem_u32(smem + L::kOffK));
+      constexpr uint32_t kStage = L::kTile >> 4;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
-        if (ok && !tc::mbar_wait(bar, parity, abort, kWaitLimit)) {
-          fail(&bars->abort, code);
-          ok = false;
-        }
+        ok = ok && warp_wait(bar, parity, abort);
+        if (!ok) fail(&bars->abort, code);
         tc::fence_after_sync();
         return ok;
       };
       auto scores = [&](uint32_t g) {
         if (!wait(&bars->k_full[g % 3], (g / 3) & 1, 5)) return;
-        mma_dims<D>(tbase + (g & 1 ? kColB : kColA), qa, ka + (g % 3) * L::kTile);
-        tc::mma_commit(&bars->s_full[g & 1]);
+        if (tc::elect_one()) {
+          mma_dims<D>(tbase + (g & 1 ? kColB : kColA), qa, kd + (g % 3) * kStage);
+          tc::mma_commit(&bars->s_full[g & 1]);
+        }
+        __syncwarp();
       };
       auto dprobs = [&](uint32_t g) {
         if (!wait(&bars->v_full[g & 1], (g >> 1) & 1, 6)) return;
-        mma_dims<D>(tbase + L::kColDp, ga, va + (g & 1) * L::kTile);
-        tc::mma_commit(&bars->dp_full);
-        tc::mma_commit(&bars->v_empty[g & 1]);
+        if (tc::elect_one()) {
+          mma_dims<D>(tbase + L::kColDp, ga, vd + (g & 1) * kStage);
+          tc::mma_commit(&bars->dp_full);
+          tc::mma_commit(&bars->v_empty[g & 1]);
+        }
+        __syncwarp();
       };
       wait(&bars->q_full, 0, 7);
       if (ok) scores(0);
@@ -673,11 +720,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&bars->ds_full, g & 1, 8)) break;
         if (g + 1 < n) dprobs(g + 1);
         if (!ok) break;
-        mma_tokens<D>(tbase + L::kColQ, tbase + (g & 1 ? kColB : kColA), ka + (g % 3) * L::kTile, g > 0);
-        tc::mma_commit(&bars->k_empty[g % 3]);
+        if (tc::elect_one()) {
+          mma_tokens<D>(tbase + L::kColQ, tbase + (g & 1 ? kColB : kColA), kt + (g % 3) * kStage, g > 0);
+          tc::mma_commit(&bars->k_empty[g % 3]);
+        }
+        __syncwarp();
       }
-      tc::mma_commit(&bars->drain);
-      tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+      if (tc::elect_one()) {
+        tc::mma_commit(&bars->drain);
+        tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ elementwise
@@ -805,8 +858,10 @@ constexpr size_t kAloneBytes = 120 * 1024;
 template <int D, bool CAP, bool BIAS>
 cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   const int qpt = kTileRows / a.G;
-  CUtensorMap mq, mg, mk, mv;
+  const int qpr = kR / a.G;
+  CUtensorMap mq, mg, mqr, mgr, mk, mv;
   if (!make_map_rows(&mq, a.q, a.qs, a, qpt) || !make_map_rows(&mg, a.dout, a.dos, a, qpt) ||
+      !make_map_rows(&mqr, a.q, a.qs, a, qpr) || !make_map_rows(&mgr, a.dout, a.dos, a, qpr) ||
       !make_map_keys(&mk, a.k, a.ks, a, kT) || !make_map_keys(&mv, a.v, a.vs, a, kT))
     return cudaErrorInvalidValue;
   {
@@ -816,7 +871,7 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const TileOrder order = tile_order(a, (a.Sk + kT - 1) / kT, a.causal);
     if ((int64_t)order.tiles * order.heads > 0x7fffffff) return cudaErrorInvalidValue;
-    kernel<<<order.tiles * order.heads, kThreads, smem, st>>>(mq, mg, mk, mv, a, qpt, order);
+    kernel<<<order.tiles * order.heads, kThreads, smem, st>>>(mqr, mgr, mk, mv, a, qpr, order);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
     __syncthreads();
   }
-  const uint32_t tbase = bars->tmem_base;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   const int2* docs = a.doc_blocks_k != nullptr ? a.doc_blocks_k + (int64_t)b * ((a.Sk + kBlock - 1) / kBlock) : nullptr;
   BlockWalk walk(docs, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
 
@@ -191,54 +191,56 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     // ------------------------------------------------------------ MMA issuer
     // Order: S_0, [S_1, PV_0], [S_2, PV_1], ..., PV_last. Products of one thread run in issue order,
     // so S_{g+2} (the buffer of S_g and P_g) always follows PV_g.
+    // The whole warp keeps step, so that what the products take is the same in all lanes; one lane issues.
     const uint32_t n = (uint32_t)walk.count(lane);
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       constexpr uint32_t idS = tc::idesc_bf16_f32(kTileRows, kBlock, 0, 0);
       constexpr uint32_t idO = tc::idesc_bf16_f32(kTileRows, D, 0, 1);
-      const uint32_t qaddr = tc::smem_u32(sQ), kaddr0 = tc::smem_u32(sK), vaddr0 = tc::smem_u32(sV);
-      auto pv = [&](uint32_t g) -> bool {
-        const int pb = g & 1;
-        if (!tc::mbar_wait(&bars->p_full[pb], (g >> 1) & 1, abort, kWaitLimit)) return false;
+      const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(sQ), 16, 1024);
+      const uint64_t kd = tc::smem_desc_sw128(tc::smem_u32(sK), 16, 1024);
+      const uint64_t vd = tc::smem_desc_sw128(tc::smem_u32(sV), L::kKVChunk, 1024);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+        ok = ok && warp_wait(bar, parity, abort);
+        if (!ok) fail(&bars->abort, code);
         tc::fence_after_sync();
-        const uint32_t vaddr = vaddr0 + pb * L::kKBytes;
-#pragma unroll
-        for (int kk = 0; kk < kBlock / 16; ++kk) {
-          const uint64_t bd = tc::smem_desc_sw128(vaddr + kk * 16 * 128, L::kKVChunk, 1024);
-          tc::mma_f16_tmem_a(tbase + L::kColO, tbase + pb * kBlock + kk * 8, bd, idO, (g == 0 && kk == 0) ? 0u : 1u);
-        }
-        tc::mma_commit(&bars->pv_done[pb]);
-        return true;
+        return ok;
       };
-      if (!tc::mbar_wait(&bars->q_full, 0, abort, kWaitLimit)) {
-        fail(&bars->abort, 5);
-      } else {
-        uint32_t g = 0;
-        for (; g < n; ++g) {
-          const int st = g % NS;
-          if (!tc::mbar_wait(&bars->k_full[st], (g / NS) & 1, abort, kWaitLimit)) {
-            fail(&bars->abort, 6);
-            break;
-          }
-          tc::fence_after_sync();
-          const uint32_t kaddr = kaddr0 + st * L::kKBytes;
+      auto pv = [&](uint32_t g) {
+        const uint32_t pb = g & 1;
+        if (!wait(&bars->p_full[pb], (g >> 1) & 1, 7)) return;
+        if (tc::elect_one()) {
+          const uint64_t bd = vd + pb * (L::kKBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const int c = kk >> 2, off = (kk & 3) * 32;
-            const uint64_t ad = tc::smem_desc_sw128(qaddr + c * L::kQChunk + off, 16, 1024);
-            const uint64_t bd = tc::smem_desc_sw128(kaddr + c * L::kKVChunk + off, 16, 1024);
-            tc::mma_f16(tbase + st * kBlock, ad, bd, idS, kk > 0 ? 1u : 0u);
-          }
-          tc::mma_commit(&bars->s_full[st]);        // also frees the K stage
-          if (g > 0 && !pv(g - 1)) {
-            fail(&bars->abort, 7);
-            break;
-          }
+          for (int kk = 0; kk < kBlock / 16; ++kk)
+            tc::mma_f16_tmem_a(tbase + L::kColO, tbase + pb * kBlock + kk * 8, bd + ((kk * 16 * 128) >> 4), idO,
+                               kk > 0 ? 1u : (uint32_t)(g > 0));
+          tc::mma_commit(&bars->pv_done[pb]);
         }
-        if (g == n && !pv(n - 1)) fail(&bars->abort, 8);
+        __syncwarp();
+      };
+      wait(&bars->q_full, 0, 5);
+      for (uint32_t g = 0; ok && g < n; ++g) {
+        const uint32_t st = g % NS;
+        if (!wait(&bars->k_full[st], (g / NS) & 1, 6)) break;
+        if (tc::elect_one()) {
+          const uint64_t bd = kd + st * (L::kKBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_f16(tbase + st * kBlock, qd + (((kk >> 2) * L::kQChunk + (kk & 3) * 32) >> 4),
+                        bd + (((kk >> 2) * L::kKVChunk + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+          tc::mma_commit(&bars->s_full[st]);        // also frees the K stage
+        }
+        __syncwarp();
+        if (g > 0) pv(g - 1);
       }
+      if (ok) pv(n - 1);
       // on every path: the products issued so far are done before TMEM is released
-      tc::mma_commit(&bars->drain);
-      tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+      if (tc::elect_one()) {
+        tc::mma_commit(&bars->drain);
+        tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ softmax and epilogue

@@ -18,6 +18,8 @@ __device__ __forceinline__ void fail(int* abort, int code) { atomicCAS(abort, 0,
 
 // A bounded wait taken by a whole warp with one outcome for all lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  // the blocking poll takes a few hundred cycles even for a phase that is complete
+  if (__all_sync(0xffffffffu, tc::mbar_test_wait(bar, parity))) return true;
   const bool ok = tc::mbar_wait(bar, parity, abort, kWaitLimit);
   return __all_sync(0xffffffffu, ok);
 }
@@ -299,9 +301,9 @@ __device__ __forceinline__ void copy_keys(unsigned char* dst, const __nv_bfloat1
   }
 }
 
-// The rows of `queries` queries from i0 of a key head's group into a tile of 128 rows, in the order of
+// The rows of `queries` queries from i0 of a key head's group into a tile of ROWS rows, in the order of
 // make_map_rows; zeros for queries at or past Sq and for padding ones.
-template <int D>
+template <int D, int ROWS>
 __device__ __forceinline__ void copy_rows(unsigned char* dst, const __nv_bfloat16* base, const fvattn_strides& s,
                                           const DenseArgs& a, int b, int h, int i0, int queries, const int32_t* doc,
                                           int me, int of) {
@@ -311,7 +313,7 @@ __device__ __forceinline__ void copy_rows(unsigned char* dst, const __nv_bfloat1
     if (i < a.Sq && (doc == nullptr || doc[i] >= 0))
       v = *reinterpret_cast<const uint4*>(base + (int64_t)b * s.b + (int64_t)(h * a.G + r % a.G) * s.h + (int64_t)i * s.s +
                                           c * 8);
-    *reinterpret_cast<uint4*>(dst + (c / 8) * kTileRows * 128 + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v;
+    *reinterpret_cast<uint4*>(dst + (c / 8) * ROWS * 128 + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v;
   }
 }
 

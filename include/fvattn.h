@@ -420,7 +420,7 @@ int fvattn_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, const
 
 /*
  * Attention over all keys.
- *  B, Hq, Hkv, Sq, Sk, d  Hq a multiple of Hkv, at most 128 times it (query head h reads key head
+ *  B, Hq, Hkv, Sq, Sk, d  Hq a multiple of Hkv, at most 64 times it (query head h reads key head
  *                    h / (Hq / Hkv)); Sq and Sk independent, >= 1; d 64 or 128.
  *  dtype             fvattn_dtype. scale: <= 0 means 1/sqrt(d).
  *  softcap           0, or c > 0: scores become c tanh(score / c).

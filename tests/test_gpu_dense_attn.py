@@ -47,7 +47,7 @@ def check(shape, dtype, cfg, seed=0, spread=1.0, grads=True, scale=None, x=None,
 SHAPES = [   # B, Hq, Hkv, Sq, Sk, d
     (1, 1, 1, 1, 1, 64), (1, 1, 1, 1, 1, 128), (2, 2, 2, 64, 64, 64), (1, 2, 2, 63, 65, 128), (1, 2, 1, 129, 127, 64),
     (2, 4, 2, 128, 128, 128), (1, 3, 1, 200, 333, 64), (1, 15, 3, 101, 140, 128), (1, 16, 1, 70, 300, 64),
-    (1, 128, 1, 3, 77, 128), (1, 100, 1, 5, 66, 64), (3, 2, 2, 257, 1, 64), (1, 1, 1, 300, 700, 128),
+    (1, 64, 1, 3, 77, 128), (1, 50, 1, 5, 66, 64), (3, 2, 2, 257, 1, 64), (1, 1, 1, 300, 700, 128),
 ]
 
 
