@@ -38,8 +38,12 @@ namespace fv {
 namespace {
 
 constexpr int kT = 128;               // rows and keys of a tile
-constexpr int kWarps = 18;            // loader, MMA, sixteen for the elementwise work: four per scheduler,
-                                      // which hide one another's waits for TMEM and the SFU
+// Loader, sixteen warps for the elementwise work (four per scheduler, which hide one another's waits for
+// TMEM and the SFU), and a warp for each kind of product. Every wait of a warp costs 100 to 300 cycles,
+// even for a barrier that is complete, and the products of a step take nearly as long to issue as to
+// run: one warp for all of them let the tensor cores run dry at each wait.
+constexpr int kWarps = 20;
+constexpr int kMmaS = 1, kMmaOut = 18, kMmaDp = 19;
 constexpr int kWork = 16;
 constexpr int kCols = kT * 4 / kWork; // columns of a score tile per thread
 constexpr int kThreads = kWarps * 32;
@@ -115,9 +119,9 @@ struct DkvLayout {
 
 struct DkvBars {
   uint64_t kv_full;
-  uint64_t q_full[kStagesQ], q_empty[kStagesQ];
-  uint64_t g_full[kStagesG], g_empty[kStagesG];      // dout
-  uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2];
+  uint64_t q_full[kStagesQ], q_empty[kStagesQ], g_full[kStagesG], g_empty[kStagesG];     // Q and dout
+  uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2];      // by parity of the step
+  uint64_t dv_done[2], dk_done[2];
   uint64_t drain;
   int doc_lo, doc_hi, doc_pad;        // documents of the keys
   uint32_t tmem_base;
@@ -155,12 +159,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars->g_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&bars->dv_done[s], 1);
+      tc::mbar_init(&bars->dk_done[s], 1);
       tc::mbar_init(&bars->s_full[s], 1);
       tc::mbar_init(&bars->dp_full[s], 1);
       tc::mbar_init(&bars->p_full[s], kWork / 2);
       tc::mbar_init(&bars->ds_full[s], kWork / 2);
     }
-    tc::mbar_init(&bars->drain, 1);
+    tc::mbar_init(&bars->drain, 3);
     bars->abort = 0;
     bars->doc_lo = 0x7fffffff;
     bars->doc_hi = -1;
@@ -217,42 +223,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t bytes = (uint32_t)(qpt * a.G) * 128 * (D / 64);
     uint32_t g = 0, q_armed = 0, g_armed = 0;      // steps whose copies were issued
-    for (int t; (t = walk.next(lane)) >= 0; ++g) {
-      const int sq = g % kStagesQ, sg = g % kStagesG, i0 = t * qpt;
-      // padding queries may hold anything: their tiles are copied by hand, with zeros for them
+    // One tensor's rows of a step into their stage.
+    auto load = [&](const CUtensorMap& map, const void* base, const fvattn_strides& st, uint64_t* full, uint64_t* empty,
+                    uint32_t empty_parity, unsigned char* dst, int i0, bool pad) -> bool {
+      if (!warp_wait(empty, empty_parity, abort)) return false;
+      if (pad) {
+        // padding queries may hold anything: copied by hand, with zeros for them
+        copy_rows<D, kR>(dst, static_cast<const __nv_bfloat16*>(base), st, a, b, h, i0, qpt, doc_q, lane, 32);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(full);
+      } else if (lane == 0) {
+        tc::mbar_expect_tx(full, bytes);
+        for (int c = 0; c < D / 64; ++c) tc::tma_load_5d(dst + c * L::kRowChunk, &map, full, c * 64, 0, i0, h, b);
+      }
+      return true;
+    };
+    bool ok = true;
+    for (int t; ok && (t = walk.next(lane)) >= 0; ++g) {
+      const uint32_t sq = g % kStagesQ, sg = g % kStagesG;
       const bool pad = tile_docs != nullptr && tile_docs[t].x < 0;
-      unsigned char *dq = smem + L::kOffQ + sq * L::kRowTile, *dg = smem + L::kOffG + sg * L::kRowTile;
-      if (!warp_wait(&bars->q_empty[sq], ((g / kStagesQ) & 1) ^ 1, abort)) {
-        fail(&bars->abort, 3);
-        break;
-      }
-      if (pad) {
-        copy_rows<D, kR>(dq, static_cast<const __nv_bfloat16*>(a.q), a.qs, a, b, h, i0, qpt, doc_q, lane, 32);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->q_full[sq]);
-      } else if (lane == 0) {
-        tc::mbar_expect_tx(&bars->q_full[sq], bytes);
-        for (int c = 0; c < D / 64; ++c)
-          tc::tma_load_5d(dq + c * L::kRowChunk, &tmQ, &bars->q_full[sq], c * 64, 0, i0, h, b);
-      }
-      q_armed = g + 1;
-      if (!warp_wait(&bars->g_empty[sg], ((g / kStagesG) & 1) ^ 1, abort)) {
-        fail(&bars->abort, 4);
-        break;
-      }
-      if (pad) {
-        copy_rows<D, kR>(dg, static_cast<const __nv_bfloat16*>(a.dout), a.dos, a, b, h, i0, qpt, doc_q, lane, 32);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->g_full[sg]);
-      } else if (lane == 0) {
-        tc::mbar_expect_tx(&bars->g_full[sg], bytes);
-        for (int c = 0; c < D / 64; ++c)
-          tc::tma_load_5d(dg + c * L::kRowChunk, &tmG, &bars->g_full[sg], c * 64, 0, i0, h, b);
-      }
-      g_armed = g + 1;
+      ok = load(tmQ, a.q, a.qs, &bars->q_full[sq], &bars->q_empty[sq], ((g / kStagesQ) & 1) ^ 1,
+                smem + L::kOffQ + sq * L::kRowTile, t * qpt, pad);
+      if (ok) q_armed = g + 1;
+      ok = ok && load(tmG, a.dout, a.dos, &bars->g_full[sg], &bars->g_empty[sg], ((g / kStagesG) & 1) ^ 1,
+                      smem + L::kOffG + sg * L::kRowTile, t * qpt, pad);
+      if (ok) g_armed = g + 1;
     }
+    if (!ok) fail(&bars->abort, 3);
     if (lane == 0) {
       // no copy may still be writing shared memory when the CTA leaves: the last of each stage
       if (kv_armed) tc::mbar_wait_drain(&bars->kv_full, 0, kWaitLimit);
@@ -261,17 +259,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t k = g_armed > kStagesG ? g_armed - kStagesG : 0; k < g_armed; ++k)
         tc::mbar_wait_drain(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, kWaitLimit);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp keeps step, so that what the products take is the same in all lanes; one lane issues.
+  } else if (warp == kMmaS || warp == kMmaOut || warp == kMmaDp) {
+    // ------------------------------------------------------------ MMA issuers
+    // Each warp keeps step as a whole, so that what the products take is the same in all lanes; one lane
+    // issues.
     if (n > 0) {
       constexpr uint32_t idS = tc::idesc_bf16_f32(kT, kR, 0, 0), idD = tc::idesc_bf16_f32(kT, D, 0, 1);
-      const uint64_t ka = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffK), 16, 1024);
-      const uint64_t va = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffV), 16, 1024);
-      const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffQ), 16, 1024);
-      const uint64_t gd = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffG), 16, 1024);
-      const uint64_t qt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffQ), L::kRowChunk, 1024);
-      const uint64_t gt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffG), L::kRowChunk, 1024);
       constexpr uint32_t kStage = L::kRowTile >> 4;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
@@ -280,59 +273,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         return ok;
       };
-      // scores^T or dP^T of a step: [128 keys x 64 rows] over the dims
-      auto over_dims = [&](uint32_t d_tmem, uint64_t key_tile, uint64_t row_tile, uint64_t* done) {
-        if (tc::elect_one()) {
+      // scores^T (K, Q) or dP^T (V, dout): [128 keys x 64 rows] over the dims, for every step
+      auto over_dims = [&](int key_off, int row_off, uint32_t stages, uint64_t* full, uint64_t* over, uint32_t col,
+                           uint64_t* done, int code) {
+        const uint64_t key_tile = tc::smem_desc_sw128(tc::smem_u32(smem + key_off), 16, 1024);
+        const uint64_t row_tile = tc::smem_desc_sw128(tc::smem_u32(smem + row_off), 16, 1024);
+        wait(&bars->kv_full, 0, code);
+        uint32_t st = 0, turn = 0;       // stage of the step and how often it has come round
+        for (uint32_t k = 0; ok && k < n; ++k) {
+          const uint32_t p = k & 1;
+          // what the step before last left in the columns has been read
+          if (k >= 2 && !wait(&over[p], ((k >> 1) & 1) ^ 1, code)) break;
+          if (!wait(&full[st], turn & 1, code + 10)) break;
+          if (tc::elect_one()) {
+            const uint64_t rd = row_tile + st * kStage;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_f16(d_tmem, key_tile + (((kk >> 2) * L::kKeyChunk + (kk & 3) * 32) >> 4),
-                        row_tile + (((kk >> 2) * L::kRowChunk + (kk & 3) * 32) >> 4), idS, kk > 0);
-          tc::mma_commit(done);
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_f16(tbase + col + p * kR, key_tile + (((kk >> 2) * L::kKeyChunk + (kk & 3) * 32) >> 4),
+                          rd + (((kk >> 2) * L::kRowChunk + (kk & 3) * 32) >> 4), idS, kk > 0);
+            tc::mma_commit(&done[p]);
+          }
+          __syncwarp();
+          if (++st == stages) {
+            st = 0;
+            ++turn;
+          }
         }
-        __syncwarp();
       };
-      // dV or dK += [128 keys x 64 rows] (bf16 in TMEM, every kCols rows over their fp32 values) x [rows x D]
-      auto over_rows = [&](uint32_t d_tmem, uint32_t w, uint64_t row_tile, uint32_t add, uint64_t* done) {
-        if (tc::elect_one()) {
+      if (warp == kMmaS) {
+        over_dims(L::kOffK, L::kOffQ, kStagesQ, bars->q_full, bars->dv_done, L::kColS, bars->s_full, 5);
+      } else if (warp == kMmaDp) {
+        over_dims(L::kOffV, L::kOffG, kStagesG, bars->g_full, bars->dk_done, L::kColDp, bars->dp_full, 6);
+      } else {
+        const uint64_t qt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffQ), L::kRowChunk, 1024);
+        const uint64_t gt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffG), L::kRowChunk, 1024);
+        // dV or dK += [128 keys x 64 rows] (bf16 in TMEM, every kCols rows over their fp32 values) x [rows x D]
+        auto over_rows = [&](uint32_t d_tmem, uint32_t w, uint64_t row_tile, uint32_t add) {
 #pragma unroll
           for (int kk = 0; kk < kR / 16; ++kk)
             tc::mma_f16_tmem_a(d_tmem, w + (kk >> 1) * kCols + (kk & 1) * 8, row_tile + ((kk * 16 * 128) >> 4), idD,
                                kk > 0 ? 1u : add);
-          tc::mma_commit(done);
+        };
+        for (uint32_t k = 0; ok && k <= n; ++k) {
+          const uint32_t p = k & 1;
+          if (k < n) {
+            // P(k) says that Q(k) has landed, not that dout(k) has
+            if (!wait(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, 7)) break;
+            if (!wait(&bars->p_full[p], (k >> 1) & 1, 8)) break;
+            if (tc::elect_one()) {
+              over_rows(tbase + L::kColV, tbase + L::kColS + p * kR, gt + (k % kStagesG) * kStage, k > 0);
+              tc::mma_commit(&bars->dv_done[p]);
+            }
+            __syncwarp();
+          }
+          if (k > 0) {
+            const uint32_t e = k - 1;
+            if (!wait(&bars->ds_full[p ^ 1], (e >> 1) & 1, 9)) break;
+            if (tc::elect_one()) {
+              over_rows(tbase + L::kColK, tbase + L::kColDp + (p ^ 1) * kR, qt + (e % kStagesQ) * kStage, e > 0);
+              tc::mma_commit(&bars->dk_done[p ^ 1]);
+              // dS(e) was made from S(e) and dP(e), so with dK(e) all four products of the step are done
+              tc::mma_commit(&bars->q_empty[e % kStagesQ]);
+              tc::mma_commit(&bars->g_empty[e % kStagesG]);
+            }
+            __syncwarp();
+          }
         }
-        __syncwarp();
-      };
-      auto scores = [&](uint32_t k) {
-        if (!wait(&bars->q_full[k % kStagesQ], (k / kStagesQ) & 1, 5)) return;
-        over_dims(tbase + L::kColS + (k & 1) * kR, ka, qd + (k % kStagesQ) * kStage, &bars->s_full[k & 1]);
-      };
-      auto dprobs = [&](uint32_t k) {
-        if (!wait(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, 6)) return;
-        over_dims(tbase + L::kColDp + (k & 1) * kR, va, gd + (k % kStagesG) * kStage, &bars->dp_full[k & 1]);
-      };
-      wait(&bars->kv_full, 0, 7);
-      if (ok) scores(0);
-      if (ok) dprobs(0);
-      if (ok && n > 1) scores(1);
-      for (uint32_t k = 0; ok && k <= n; ++k) {
-        if (k < n) {
-          if (!wait(&bars->p_full[k & 1], (k >> 1) & 1, 8)) break;
-          over_rows(tbase + L::kColV, tbase + L::kColS + (k & 1) * kR, gt + (k % kStagesG) * kStage, k > 0,
-                    &bars->g_empty[k % kStagesG]);
-          if (k + 2 < n) scores(k + 2);
-        }
-        if (k > 0) {
-          if (!wait(&bars->ds_full[(k - 1) & 1], ((k - 1) >> 1) & 1, 9)) break;
-          over_rows(tbase + L::kColK, tbase + L::kColDp + ((k - 1) & 1) * kR, qt + ((k - 1) % kStagesQ) * kStage, k > 1,
-                    &bars->q_empty[(k - 1) % kStagesQ]);
-        }
-        if (k + 1 < n) dprobs(k + 1);
       }
       // on every path: the products issued so far are done before TMEM is read or released
-      if (tc::elect_one()) {
-        tc::mma_commit(&bars->drain);
-        tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
-      }
+      if (tc::elect_one()) tc::mma_commit(&bars->drain);
+      __syncwarp();
+      if (lane == 0) tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
       __syncwarp();
     }
   } else {
@@ -551,7 +562,8 @@ struct DqLayout : BwdLayout<D> {
 struct DqBars {
   uint64_t q_full;
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
-  uint64_t s_full[2], dp_full, ds_full;
+  uint64_t s_full[2], dq_done[2];      // by parity of the step
+  uint64_t dp_full, ds_full;
   uint64_t drain;
   int doc_lo, doc_hi;
   uint32_t tmem_base;
@@ -590,10 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars->v_full[s], 1);
       tc::mbar_init(&bars->v_empty[s], 1);
       tc::mbar_init(&bars->s_full[s], 1);
+      tc::mbar_init(&bars->dq_done[s], 1);
     }
     tc::mbar_init(&bars->dp_full, 1);
     tc::mbar_init(&bars->ds_full, kWork);
-    tc::mbar_init(&bars->drain, 1);
+    tc::mbar_init(&bars->drain, 2);
     bars->abort = 0;
     bars->doc_lo = 0x7fffffff;
     bars->doc_hi = -1;
@@ -624,25 +637,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ loader
-    bool q_armed = false;
-    int k_par[3] = {-1, -1, -1}, v_par[2] = {-1, -1};
-    if (lane == 0 && n > 0) {
-      tc::mbar_expect_tx(&bars->q_full, 2 * (uint32_t)(qpt * a.G) * 128 * (D / 64));
-      q_armed = true;
-      for (int c = 0; c < D / 64; ++c) {
-        tc::tma_load_5d(smem + L::kOffQ + c * L::kChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
-        tc::tma_load_5d(smem + L::kOffG + c * L::kChunk, &tmG, &bars->q_full, c * 64, 0, i0, h, b);
-      }
-    }
-    uint32_t g = 0;
-    for (int j; (j = walk.next(lane)) >= 0; ++g) {
-      const int sk = g % 3, sv = g & 1;
-      const uint32_t pk = (g / 3) & 1, pv = (g >> 1) & 1;
+    uint32_t g = 0, k_armed = 0, v_armed = 0;      // steps whose copies were issued
+    bool q_armed = false, ok = true;
+    for (int j; ok && (j = walk.next(lane)) >= 0; ++g) {
+      const uint32_t sk = g % 3, sv = g & 1;
       unsigned char* dk = smem + L::kOffK + sk * L::kTile;
-      if (!warp_wait(&bars->k_empty[sk], pk ^ 1, abort)) {
-        fail(&bars->abort, 3);
-        break;
+      if (g == 0) {
+        if (lane == 0) {
+          tc::mbar_expect_tx(&bars->q_full, 2 * (uint32_t)(qpt * a.G) * 128 * (D / 64));
+          for (int c = 0; c < D / 64; ++c) {
+            tc::tma_load_5d(smem + L::kOffQ + c * L::kChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
+            tc::tma_load_5d(smem + L::kOffG + c * L::kChunk, &tmG, &bars->q_full, c * 64, 0, i0, h, b);
+          }
+        }
+        q_armed = true;
       }
+      ok = warp_wait(&bars->k_empty[sk], ((g / 3) & 1) ^ 1, abort);
+      if (!ok) break;
       // keys that do not exist: zeros, whatever their memory holds (0 * NaN would reach dQ)
       const bool dirty = (seq.kv < a.Sk && (j + 1) * kT > seq.kv) || (doc_k != nullptr && walk.docs[j].x < 0);
       if (dirty) {
@@ -656,37 +667,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < D / 64; ++c)
           tc::tma_load_4d(dk + c * L::kChunk, &tmK, &bars->k_full[sk], c * 64, j * kT, h, b);
       }
-      k_par[0] = sk == 0 ? (int)pk : k_par[0];
-      k_par[1] = sk == 1 ? (int)pk : k_par[1];
-      k_par[2] = sk == 2 ? (int)pk : k_par[2];
-      if (!warp_wait(&bars->v_empty[sv], pv ^ 1, abort)) {
-        fail(&bars->abort, 4);
-        break;
-      }
+      k_armed = g + 1;
+      ok = warp_wait(&bars->v_empty[sv], ((g >> 1) & 1) ^ 1, abort);
+      if (!ok) break;
       if (lane == 0) {
         tc::mbar_expect_tx(&bars->v_full[sv], L::kTile);
         for (int c = 0; c < D / 64; ++c)
           tc::tma_load_4d(smem + L::kOffV + sv * L::kTile + c * L::kChunk, &tmV, &bars->v_full[sv], c * 64, j * kT, h, b);
       }
-      v_par[0] = sv == 0 ? (int)pv : v_par[0];
-      v_par[1] = sv == 1 ? (int)pv : v_par[1];
+      v_armed = g + 1;
     }
+    if (!ok) fail(&bars->abort, 3);
     if (lane == 0) {
+      // no copy may still be writing shared memory when the CTA leaves: the last of each stage
       if (q_armed) tc::mbar_wait_drain(&bars->q_full, 0, kWaitLimit);
-#pragma unroll
-      for (int s = 0; s < 3; ++s)
-        if (k_par[s] >= 0) tc::mbar_wait_drain(&bars->k_full[s], (uint32_t)k_par[s], kWaitLimit);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (v_par[s] >= 0) tc::mbar_wait_drain(&bars->v_full[s], (uint32_t)v_par[s], kWaitLimit);
+      for (uint32_t k = k_armed > 3 ? k_armed - 3 : 0; k < k_armed; ++k)
+        tc::mbar_wait_drain(&bars->k_full[k % 3], (k / 3) & 1, kWaitLimit);
+      for (uint32_t k = v_armed > 2 ? v_armed - 2 : 0; k < v_armed; ++k)
+        tc::mbar_wait_drain(&bars->v_full[k & 1], (k >> 1) & 1, kWaitLimit);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp keeps step, so that what the products take is the same in all lanes; one lane issues.
-    if (n > 0) {
-      const uint64_t qa = desc_dims(tc::smem_u32(smem + L::kOffQ)), ga = desc_dims(tc::smem_u32(smem + L::kOffG));
-      const uint64_t kd = desc_dims(tc::smem_u32(smem + L::kOffK)), vd = desc_dims(tc::smem_u32(smem + L::kOffV));
-      const uint64_t kt = desc_tokens(tc::smem_u32(smem + L::kOffK));
+  } else if (warp == kMmaS || warp == kMmaOut || warp == kMmaDp) {
+    // ------------------------------------------------------------ MMA issuers
+    // Each warp keeps step as a whole, so that what the products take is the same in all lanes; one lane
+    // issues. One warp makes dP and dQ, in this order: dS(g+1) waits for dP(g+1).
+    if (n > 0 && warp != kMmaDp) {
       constexpr uint32_t kStage = L::kTile >> 4;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
@@ -695,41 +699,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         return ok;
       };
-      auto scores = [&](uint32_t g) {
-        if (!wait(&bars->k_full[g % 3], (g / 3) & 1, 5)) return;
-        if (tc::elect_one()) {
-          mma_dims<D>(tbase + (g & 1 ? kColB : kColA), qa, kd + (g % 3) * kStage);
-          tc::mma_commit(&bars->s_full[g & 1]);
-        }
-        __syncwarp();
-      };
-      auto dprobs = [&](uint32_t g) {
-        if (!wait(&bars->v_full[g & 1], (g >> 1) & 1, 6)) return;
-        if (tc::elect_one()) {
-          mma_dims<D>(tbase + L::kColDp, ga, vd + (g & 1) * kStage);
-          tc::mma_commit(&bars->dp_full);
-          tc::mma_commit(&bars->v_empty[g & 1]);
-        }
-        __syncwarp();
-      };
       wait(&bars->q_full, 0, 7);
-      if (ok) scores(0);
-      if (ok) dprobs(0);
-      for (uint32_t g = 0; ok && g < n; ++g) {
-        if (g + 1 < n) scores(g + 1);
-        if (!wait(&bars->ds_full, g & 1, 8)) break;
-        if (g + 1 < n) dprobs(g + 1);
-        if (!ok) break;
-        if (tc::elect_one()) {
-          mma_tokens<D>(tbase + L::kColQ, tbase + (g & 1 ? kColB : kColA), kt + (g % 3) * kStage, g > 0);
-          tc::mma_commit(&bars->k_empty[g % 3]);
+      uint32_t st = 0, turn = 0;       // K's stage of the step and how often it has come round
+      auto advance = [&] {
+        if (++st == L::kStagesK) {
+          st = 0;
+          ++turn;
         }
-        __syncwarp();
+      };
+      if (warp == kMmaS) {
+        const uint64_t qa = desc_dims(tc::smem_u32(smem + L::kOffQ)), kd = desc_dims(tc::smem_u32(smem + L::kOffK));
+        for (uint32_t g = 0; ok && g < n; ++g) {
+          // dS of the step before last has been read
+          if (g >= 2 && !wait(&bars->dq_done[g & 1], ((g >> 1) & 1) ^ 1, 4)) break;
+          if (!wait(&bars->k_full[st], turn & 1, 5)) break;
+          if (tc::elect_one()) {
+            mma_dims<D>(tbase + (g & 1 ? kColB : kColA), qa, kd + st * kStage);
+            tc::mma_commit(&bars->s_full[g & 1]);
+          }
+          __syncwarp();
+          advance();
+        }
+      } else {
+        const uint64_t ga = desc_dims(tc::smem_u32(smem + L::kOffG)), vd = desc_dims(tc::smem_u32(smem + L::kOffV));
+        const uint64_t kt = desc_tokens(tc::smem_u32(smem + L::kOffK));
+        for (uint32_t g = 0; ok && g <= n; ++g) {
+          if (g < n && !wait(&bars->v_full[g & 1], (g >> 1) & 1, 6)) break;
+          // dP(g) may overwrite dP(g-1) once dS(g-1) has been made from it
+          if (g > 0 && !wait(&bars->ds_full, (g - 1) & 1, 8)) break;
+          if (g < n) {
+            if (tc::elect_one()) {
+              mma_dims<D>(tbase + L::kColDp, ga, vd + (g & 1) * kStage);
+              tc::mma_commit(&bars->dp_full);
+              tc::mma_commit(&bars->v_empty[g & 1]);
+            }
+            __syncwarp();
+          }
+          if (g > 0) {
+            const uint32_t e = g - 1;
+            if (tc::elect_one()) {
+              mma_tokens<D>(tbase + L::kColQ, tbase + (e & 1 ? kColB : kColA), kt + st * kStage, e > 0);
+              tc::mma_commit(&bars->dq_done[e & 1]);
+              tc::mma_commit(&bars->k_empty[st]);
+            }
+            __syncwarp();
+            advance();
+          }
+        }
       }
-      if (tc::elect_one()) {
-        tc::mma_commit(&bars->drain);
-        tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
-      }
+      if (tc::elect_one()) tc::mma_commit(&bars->drain);
+      __syncwarp();
+      if (lane == 0) tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
       __syncwarp();
     }
   } else {
