@@ -70,6 +70,28 @@ __device__ inline int debug_row_check(const int32_t* row_ptr, const int32_t* col
 }
 #endif
 
+// A kernel launched by launch_after_previous may start while the one before it on its stream still
+// runs; it waits here until that has ended and its writes are visible, before it touches anything that
+// the other may write or read. allow_next_grid, in the one before, lets it start early.
+__device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_after_previous(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                                  A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 __device__ __forceinline__ uint32_t lanemask_lt() {
   uint32_t m;
   asm volatile("mov.u32 %0, %%lanemask_lt;" : "=r"(m));

@@ -161,6 +161,7 @@ __device__ __forceinline__ float half_warp_sum(float v) {
 // grid: (row tiles * splits, Hkv, B)
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) dense_fwd_kernel(const DenseArgs a) {
+  allow_next_grid();
   extern __shared__ float sm[];
   float *sQ = sm, *sK = sQ + Tile<D>::kFloats, *sV = sK + Tile<D>::kFloats, *sP = sV + Tile<D>::kFloats;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_kernel(const DenseArgs a) 
 // Joins the splits of a row: weights exp(lse_s - max) in a fixed order. One warp per row.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) dense_combine_kernel(const DenseArgs a) {
+  wait_for_previous_grid();
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
   const int64_t flat = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -546,14 +548,9 @@ cudaError_t launch_dense_docs(const int32_t* doc, int2* blocks, int B, int S, in
 }
 
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == FVATTN_F32) {
-    if (a.d == 128) dense_combine_kernel<float, 128><<<warp_rows(a), kThreads, 0, st>>>(a);
-    else dense_combine_kernel<float, 64><<<warp_rows(a), kThreads, 0, st>>>(a);
-  } else {
-    if (a.d == 128) dense_combine_kernel<__nv_bfloat16, 128><<<warp_rows(a), kThreads, 0, st>>>(a);
-    else dense_combine_kernel<__nv_bfloat16, 64><<<warp_rows(a), kThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  auto go = [&](auto kernel) { return launch_after_previous(kernel, dim3(warp_rows(a)), kThreads, 0, st, a); };
+  if (dtype == FVATTN_F32) return a.d == 128 ? go(dense_combine_kernel<float, 128>) : go(dense_combine_kernel<float, 64>);
+  return a.d == 128 ? go(dense_combine_kernel<__nv_bfloat16, 128>) : go(dense_combine_kernel<__nv_bfloat16, 64>);
 }
 
 cudaError_t launch_dense_delta(const DenseArgs& a, int dtype, cudaStream_t st) {

@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   unsigned char* sV = smem + L::kOffV;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
+  allow_next_grid();
 
   int x, bh;
   tile_of(order, blockIdx.x, x, bh);

@@ -25,22 +25,43 @@ namespace fv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;          // heads in flight per thread
+constexpr int kUnroll = 4;          // heads in flight per thread (forward; both inputs of two heads backward)
+constexpr int kSms = 148;
 constexpr int kBadPosition = 201;   // status detail: a position outside the tables
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// Eight elements as loaded, and as fp32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
   }
+  __device__ __forceinline__ void to(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void to(float (&x)[8]) const {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  Raw8<T> r;
+  r.load(p);
+  r.to(x);
 }
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -174,32 +195,37 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs a, c
   if (bad && live && a.status != nullptr) report_error(a.status, FVATTN_ERR_INVALID, kBadPosition);
 
   for (int h = ch.h0; h < ch.h1; h += kUnroll) {
-    float v[kUnroll][8];
+    Raw8<T> raw[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      load8(x + (int64_t)min(h + u, ch.h1 - 1) * xs.h, v[u]);
+      if (h + u < ch.h1) raw[u].load(x + (int64_t)(h + u) * xs.h);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
+      if (h + u >= ch.h1) break;          // the same for the whole CTA
+      float v[8];
+      raw[u].to(v);
       float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += v[u][i] * v[u][i];
+      for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
       const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + s.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * r * w[i];
-      if (s.rot > 0) turn.template apply<1>(v[u], lane);
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
+      if (s.rot > 0) turn.template apply<1>(v, lane);
       if (bad) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = __int_as_float(0x7fffffff);   // a position outside the tables: NaN
+        for (int i = 0; i < 8; ++i) v[i] = __int_as_float(0x7fffffff);   // a position outside the tables: NaN
       }
-      if (live && h + u < ch.h1) store8(y + (int64_t)(h + u) * ys.h, v[u]);
+      if (live) store8(y + (int64_t)(h + u) * ys.h, v);
     }
   }
 }
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const QkNormArgs a, const fvattn_qk_shape s, int per) {
+__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const QkNormArgs a, const fvattn_qk_shape s, int per,
+                                                               int walk) {
   constexpr int LPR = D / 8, TOK = kThreads / LPR, U = 2;
   __shared__ float sw[TOK][D];
+  allow_next_grid();
   const int lane = threadIdx.x & 31, l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
   const Chunk ch = chunk_of(blockIdx.y, (int)s.Hq, (int)s.Hk, per);
   const int64_t ntok = s.B * s.S;
@@ -209,7 +235,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const QkNormArgs 
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[i] = 0.f;
 
-  for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < ntok; t0 += (int64_t)gridDim.x * TOK) {
+  const int64_t t1 = (int64_t)(blockIdx.x + 1) * walk * TOK;
+  for (int64_t t0 = (int64_t)blockIdx.x * walk * TOK; t0 < t1 && t0 < ntok; t0 += TOK) {
     const int64_t t = t0 + grp;
     const bool live = t < ntok;
     const int64_t tt = live ? t : 0;
@@ -230,32 +257,35 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const QkNormArgs 
     }
     if (bad && live && a.status != nullptr) report_error(a.status, FVATTN_ERR_INVALID, kBadPosition);
     for (int h = ch.h0; h < ch.h1; h += U) {
-      float v[U][8], g[U][8];
+      Raw8<T> rx[U], rg[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t hh = min(h + u, ch.h1 - 1);
-        load8(x + hh * xs.h, v[u]);
-        load8(gy + hh * gs.h, g[u]);
+        if (h + u >= ch.h1) break;        // the same for the whole CTA
+        rx[u].load(x + (int64_t)(h + u) * xs.h);
+        rg[u].load(gy + (int64_t)(h + u) * gs.h);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool write = live && h + u < ch.h1;
-        if (s.rot > 0) turn.template apply<-1>(g[u], lane);
+        if (h + u >= ch.h1) break;
+        float v[8], g[8];
+        rx[u].to(v);
+        rg[u].to(g);
+        if (s.rot > 0) turn.template apply<-1>(g, lane);
         float ss = 0.f, sg = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          ss += v[u][i] * v[u][i];
-          sg += g[u][i] * w[i] * v[u][i];
+          ss += v[i] * v[i];
+          sg += g[i] * w[i] * v[i];
         }
         const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + s.eps);
         const float m = row_sum<LPR>(sg) * (1.f / D) * r * r;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (bad) g[u][i] = __int_as_float(0x7fffffff);
-          if (write) dw[i] += g[u][i] * (v[u][i] * r);
-          v[u][i] = r * (g[u][i] * w[i] - v[u][i] * m);
+          if (bad) g[i] = __int_as_float(0x7fffffff);
+          if (live) dw[i] += g[i] * (v[i] * r);
+          v[i] = r * (g[i] * w[i] - v[i] * m);
         }
-        if (write) store8(dx + (int64_t)(h + u) * ds.h, v[u]);
+        if (live) store8(dx + (int64_t)(h + u) * ds.h, v);
       }
     }
   }
@@ -276,33 +306,35 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const QkNormArgs 
 }
 
 // dw[c] = sum over the parts of column c, in 64 bits and in a fixed order. blockIdx.y: queries, keys.
-__global__ void __launch_bounds__(kThreads) qk_norm_sum_kernel(const QkNormArgs a, int D, int64_t parts_q,
-                                                               int64_t parts_k) {
-  __shared__ double ss[kThreads / 8][8];
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) qk_norm_sum_kernel(const QkNormArgs a, int D, int64_t parts_q,
+                                                                  int64_t parts_k) {
+  __shared__ double ss[kSumThreads / 8][8];
+  wait_for_previous_grid();
   const int col = blockIdx.x * 8 + (threadIdx.x & 7), k = threadIdx.x >> 3;
   const bool key = blockIdx.y == 1;
   float* out = key ? a.dwk : a.dwq;
   if (out == nullptr) return;
-  const float* p = a.parts + (key ? parts_q * D : 0);
+  const float* p = a.parts + (key ? parts_q * D : 0) + col;
   const int64_t n = key ? parts_k : parts_q;
   double acc = 0.0;
-  for (int64_t r = k; r < n; r += kThreads / 8) acc += (double)p[r * D + col];
+#pragma unroll 4
+  for (int64_t r = k; r < n; r += kSumThreads / 8) acc += (double)p[r * D];
   ss[k][threadIdx.x & 7] = acc;
-  __syncthreads();
-  if (k == 0) {
-    for (int i = 1; i < kThreads / 8; ++i) acc += ss[i][threadIdx.x & 7];
-    out[col] = (float)acc;
+  for (int half = kSumThreads / 16; half > 0; half >>= 1) {
+    __syncthreads();
+    if (k < half) ss[k][threadIdx.x & 7] += ss[k + half][threadIdx.x & 7];
   }
+  if (k == 0) out[col] = (float)ss[0][threadIdx.x & 7];
 }
 
-// Heads per CTA: all of a tensor's heads when the token tiles alone fill the GPU (a token's
-// cosines and sines are then loaded once), fewer when there are few tokens.
-constexpr int kSms = 148;
-int heads_per_cta(const fvattn_qk_shape& s, int64_t tiles, int most) {
+// Heads per CTA: all of a tensor's heads when the token tiles alone make several CTAs for every SM (a
+// token's cosines and sines are then loaded once for all), in groups of kUnroll fewer otherwise.
+int heads_per_cta(const fvattn_qk_shape& s, int64_t tiles) {
   const int64_t want = (int64_t)kSms * 8;
-  int per = most;
-  while (per > kUnroll && tiles * ((s.Hq + per - 1) / per + (s.Hk + per - 1) / per) < want) per = (per + 1) / 2;
-  return per < 1 ? 1 : per;
+  int per = (int)((imax(s.Hq, s.Hk) + kUnroll - 1) / kUnroll) * kUnroll;
+  while (per > kUnroll && tiles * ((s.Hq + per - 1) / per + (s.Hk + per - 1) / per) < want) per -= kUnroll;
+  return per;
 }
 
 int64_t tok_tiles(const fvattn_qk_shape& s) {
@@ -310,17 +342,20 @@ int64_t tok_tiles(const fvattn_qk_shape& s) {
   return (s.B * s.S + tok - 1) / tok;
 }
 
+// The gradients' CTAs: groups of 2 kUnroll heads, and of `walk` token tiles so that the partial sums of
+// the weights' gradients stay few.
 struct BwdPlan {
-  int per, gx;
+  int per, walk, gx;
   int64_t parts_q, parts_k;
 };
 BwdPlan bwd_plan(const fvattn_qk_shape& s) {
   BwdPlan p;
   const int64_t tiles = tok_tiles(s);
-  p.per = heads_per_cta(s, tiles, (int)imax<int64_t>(s.Hq, s.Hk));
+  p.per = 2 * kUnroll;
+  while (p.per > 1 && tiles * ((s.Hq + p.per - 1) / p.per + (s.Hk + p.per - 1) / p.per) < (int64_t)kSms * 4) p.per >>= 1;
   const int64_t nq = (s.Hq + p.per - 1) / p.per, nk = (s.Hk + p.per - 1) / p.per;
-  // a few CTAs per SM in all, each walking over token tiles: few partial sums are written
-  p.gx = (int)imin<int64_t>(tiles, imax<int64_t>(1, (int64_t)kSms * 8 / (nq + nk)));
+  p.walk = (int)imax<int64_t>(1, tiles * (nq + nk) / ((int64_t)kSms * 32));
+  p.gx = (int)((tiles + p.walk - 1) / p.walk);
   p.parts_q = nq * p.gx;
   p.parts_k = nk * p.gx;
   return p;
@@ -329,7 +364,7 @@ BwdPlan bwd_plan(const fvattn_qk_shape& s) {
 template <typename T, int D>
 cudaError_t fwd_d(const QkNormArgs& a, const fvattn_qk_shape& s, cudaStream_t st) {
   const int64_t tiles = tok_tiles(s);
-  const int per = heads_per_cta(s, tiles, (int)imax<int64_t>(s.Hq, s.Hk));
+  const int per = heads_per_cta(s, tiles);
   const dim3 grid((unsigned)tiles, (unsigned)((s.Hq + per - 1) / per + (s.Hk + per - 1) / per));
   if (s.interleaved)
     qk_norm_kernel<T, D, true><<<grid, kThreads, 0, st>>>(a, s, per);
@@ -343,13 +378,12 @@ cudaError_t bwd_d(const QkNormArgs& a, const fvattn_qk_shape& s, cudaStream_t st
   const BwdPlan p = bwd_plan(s);
   const dim3 grid((unsigned)p.gx, (unsigned)((p.parts_q + p.parts_k) / p.gx));
   if (s.interleaved)
-    qk_norm_bwd_kernel<T, D, true><<<grid, kThreads, 0, st>>>(a, s, p.per);
+    qk_norm_bwd_kernel<T, D, true><<<grid, kThreads, 0, st>>>(a, s, p.per, p.walk);
   else
-    qk_norm_bwd_kernel<T, D, false><<<grid, kThreads, 0, st>>>(a, s, p.per);
+    qk_norm_bwd_kernel<T, D, false><<<grid, kThreads, 0, st>>>(a, s, p.per, p.walk);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (a.dwq == nullptr && a.dwk == nullptr)) return e;
-  qk_norm_sum_kernel<<<dim3(D / 8, 2), kThreads, 0, st>>>(a, D, p.parts_q, p.parts_k);
-  return cudaGetLastError();
+  return launch_after_previous(qk_norm_sum_kernel, dim3(D / 8, 2), kSumThreads, 0, st, a, D, p.parts_q, p.parts_k);
 }
 
 }  // namespace
