@@ -25,7 +25,7 @@ namespace fv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;          // heads in flight per thread (forward; both inputs of two heads backward)
+constexpr int kUnroll = 4;          // heads in flight per thread
 constexpr int kSms = 148;
 constexpr int kBadPosition = 201;   // status detail: a position outside the tables
 
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs a, c
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const QkNormArgs a, const fvattn_qk_shape s, int per,
                                                                int walk) {
-  constexpr int LPR = D / 8, TOK = kThreads / LPR, U = 2;
+  constexpr int LPR = D / 8, TOK = kThreads / LPR, U = 4;
   __shared__ float sw[TOK][D];
   allow_next_grid();
   const int lane = threadIdx.x & 31, l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
@@ -342,7 +342,7 @@ int64_t tok_tiles(const fvattn_qk_shape& s) {
   return (s.B * s.S + tok - 1) / tok;
 }
 
-// The gradients' CTAs: groups of 2 kUnroll heads, and of `walk` token tiles so that the partial sums of
+// The gradients' CTAs: groups of 4 kUnroll heads, and of `walk` token tiles so that the partial sums of
 // the weights' gradients stay few.
 struct BwdPlan {
   int per, walk, gx;
@@ -351,8 +351,8 @@ struct BwdPlan {
 BwdPlan bwd_plan(const fvattn_qk_shape& s) {
   BwdPlan p;
   const int64_t tiles = tok_tiles(s);
-  p.per = 2 * kUnroll;
-  while (p.per > 1 && tiles * ((s.Hq + p.per - 1) / p.per + (s.Hk + p.per - 1) / p.per) < (int64_t)kSms * 4) p.per >>= 1;
+  p.per = 4 * kUnroll;
+  while (p.per > 1 && tiles * ((s.Hq + p.per - 1) / p.per + (s.Hk + p.per - 1) / p.per) < (int64_t)kSms * 2) p.per >>= 1;
   const int64_t nq = (s.Hq + p.per - 1) / p.per, nk = (s.Hk + p.per - 1) / p.per;
   p.walk = (int)imax<int64_t>(1, tiles * (nq + nk) / ((int64_t)kSms * 32));
   p.gx = (int)((tiles + p.walk - 1) / p.walk);
