@@ -27,7 +27,7 @@ DEBUG_LIB = os.path.join(PKG, "libfvattn_debug.so")
 
 SOURCES = ["api.cu", "route.cu", "attn_f32.cu", "attn_tc.cu", "route_static.cu", "balance.cu", "score_tc.cu",
            "api_layer.cu", "qk_norm.cu", "dense_f32.cu", "dense_tc.cu",
-           "dense_bwd_tc.cu"]
+           "dense_bwd_tc.cu", "dense_few.cu"]
 HEADERS = ["common.cuh", "route.cuh", "route_dev.cuh", "tc_ptx.cuh", "tmap.cuh", "qk_norm.cuh",
            "dense.cuh", "dense_tc.cuh"]
 

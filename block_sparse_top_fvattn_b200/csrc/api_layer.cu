@@ -111,7 +111,7 @@ DenseArgs dense_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
   a.dqs = canonical(s->dq, s->B, s->Hq, s->Sq, s->d);
   a.dks = canonical(s->dk, s->B, s->Hkv, s->Sk, s->d);
   a.dvs = canonical(s->dv, s->B, s->Hkv, s->Sk, s->d);
-  a.splits = 1;
+  a.splits = a.cluster = a.parts = 1;
   a.split_keys = (a.Sk + kBlock - 1) / kBlock * kBlock;
   return a;
 }
@@ -120,16 +120,34 @@ DenseArgs dense_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
 // idle and each split still has a few blocks of keys to work on.
 constexpr int kSlots = 2 * 148;
 constexpr int kMinSplitKeys = 256;
-void plan_splits(DenseArgs& a, int tile_rows_queries) {
-  const int64_t tiles = ((int64_t)a.Sq + tile_rows_queries - 1) / tile_rows_queries * a.Hkv * a.B;
-  if (tiles * 2 > kSlots) return;
-  const int64_t want = kSlots / tiles;
-  const int64_t most = ((int64_t)a.Sk + kMinSplitKeys - 1) / kMinSplitKeys;
-  const int64_t n = imax<int64_t>(1, imin(want, most));
+constexpr int kMostCluster = 8;
+void split_in(DenseArgs& a, int64_t n) {
   const int64_t blocks = ((int64_t)a.Sk + kBlock - 1) / kBlock;
   const int64_t per = (blocks + n - 1) / n;
   a.split_keys = (int)(per * kBlock);
   a.splits = (int)((blocks + per - 1) / per);
+}
+void plan_splits(DenseArgs& a, int tile_rows_queries) {
+  const int64_t tiles = ((int64_t)a.Sq + tile_rows_queries - 1) / tile_rows_queries * a.Hkv * a.B;
+  if (tiles * 2 <= kSlots) {
+    const int64_t most = ((int64_t)a.Sk + kMinSplitKeys - 1) / kMinSplitKeys;
+    split_in(a, imax<int64_t>(1, imin(kSlots / tiles, most)));
+  }
+  a.parts = a.splits;
+}
+// For few rows: two waves of CTAs (the second evens out sequences of unequal length), of two blocks of keys
+// at least; a cluster of a power of two up to its most, and whole clusters beyond.
+void plan_few(DenseArgs& a) {
+  const int64_t heads = (int64_t)a.B * a.Hkv, blocks = ((int64_t)a.Sk + kBlock - 1) / kBlock;
+  const int64_t n = imax<int64_t>(1, imin((2 * kSlots + heads - 1) / heads, (blocks + 1) / 2));
+  a.cluster = 1;
+  while (a.cluster < kMostCluster && a.cluster < n) a.cluster *= 2;
+  split_in(a, n <= kMostCluster ? n : (n + kMostCluster / 2) / kMostCluster * kMostCluster);
+  a.splits = (a.splits + a.cluster - 1) / a.cluster * a.cluster;
+  a.parts = a.splits / a.cluster;
+}
+bool few_rows(const DenseArgs& a, int dtype) {
+  return dtype == FVATTN_BF16 && (int64_t)a.Sq * a.G <= kFewRows && (int64_t)a.B * a.Hkv <= 65535;
 }
 
 size_t take(size_t& off, size_t bytes) {
@@ -148,9 +166,9 @@ DenseWs fwd_ws(const DenseArgs& a, int dtype) {
   DenseWs w{};
   size_t off = 0;
   const size_t rows = (size_t)a.B * a.Hq * a.Sq;
-  if (a.splits > 1) {
-    w.part_o = take(off, rows * a.splits * a.d * sizeof(float));
-    w.part_lse = take(off, rows * a.splits * sizeof(float));
+  if (a.parts > 1) {
+    w.part_o = take(off, rows * a.parts * a.d * sizeof(float));
+    w.part_lse = take(off, rows * a.parts * sizeof(float));
   }
   if (dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) w.docs_k = take(off, doc_bytes(a.B, a.Sk, kBlock));
   w.total = off;
@@ -173,7 +191,10 @@ DenseWs bwd_ws(const DenseArgs& a, int dtype) {
 
 DenseArgs fwd_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
   DenseArgs a = dense_args(s, m);
-  plan_splits(a, s->dtype == FVATTN_F32 ? imax(1, 64 / a.G) : kTileRows / a.G);
+  if (few_rows(a, s->dtype))
+    plan_few(a);
+  else
+    plan_splits(a, s->dtype == FVATTN_F32 ? imax(1, 64 / a.G) : kTileRows / a.G);
   return a;
 }
 
@@ -271,7 +292,7 @@ int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_
   a.rest = rest;
   a.lse = lse;
   a.status = status;
-  if (a.splits > 1) {
+  if (a.parts > 1) {
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
     a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   }
@@ -281,8 +302,11 @@ int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_
     a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
     e = launch_dense_docs(a.mask.doc_k, a.doc_blocks_k, a.B, a.Sk, kBlock, s);
   }
-  if (e == cudaSuccess) e = shape->dtype == FVATTN_BF16 ? launch_dense_tc(a, s) : launch_dense_f32(a, s);
-  if (e == cudaSuccess && a.splits > 1) e = launch_dense_combine(a, shape->dtype, s);
+  if (e == cudaSuccess)
+    e = shape->dtype == FVATTN_F32 ? launch_dense_f32(a, s)
+        : few_rows(a, shape->dtype) ? launch_dense_few(a, s)
+                                    : launch_dense_tc(a, s);
+  if (e == cudaSuccess && a.parts > 1) e = launch_dense_combine(a, shape->dtype, s);
   return cuda_status(e);
 }
 

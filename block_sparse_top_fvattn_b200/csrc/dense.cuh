@@ -27,7 +27,8 @@ struct DenseArgs {
   int causal;
   float scale, cap;
   int splits, split_keys;         // forward: the keys in `splits` ranges of split_keys (a multiple of 64)
-  float *part_o, *part_lse;       // splits > 1: [splits][B][Hq][Sq][d] and [splits][B][Hq][Sq]
+  int cluster, parts;             // ranges joined within a cluster; what is left to join through memory
+  float *part_o, *part_lse;       // parts > 1: [parts][B][Hq][Sq][d] and [parts][B][Hq][Sq]
   float* delta;                   // backward: [B][Hq][Sq], sum_d out * dout
   // Documents of blocks of tokens (dense_doc_kernel), null without documents: of the keys in blocks of
   // 64 (forward) or 128 (backward), of the queries in steps of dK and dV (backward).
@@ -82,6 +83,8 @@ __device__ __forceinline__ DenseRow dense_row(const DenseArgs& a, const DenseSeq
 cudaError_t launch_dense_docs(const int32_t* doc, int2* blocks, int B, int S, int block, cudaStream_t st);
 cudaError_t launch_dense_bwd_tc(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_tc(const DenseArgs& a, cudaStream_t st);
+cudaError_t launch_dense_few(const DenseArgs& a, cudaStream_t st);
+constexpr int kFewRows = 16;      // the most rows of a key head that launch_dense_few takes
 cudaError_t launch_dense_f32(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_dense_delta(const DenseArgs& a, int dtype, cudaStream_t st);

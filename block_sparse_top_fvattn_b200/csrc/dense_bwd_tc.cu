@@ -128,6 +128,8 @@ struct DkvBars {
   int abort;
 };
 
+static_assert(sizeof(DkvBars) <= 512, "the barriers fit their place");
+
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
@@ -569,6 +571,8 @@ struct DqBars {
   uint32_t tmem_base;
   int abort;
 };
+
+static_assert(sizeof(DqBars) <= 256, "the barriers fit their place");
 
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)

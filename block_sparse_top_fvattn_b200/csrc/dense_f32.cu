@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) dense_combine_kernel(const DenseArgs
   const int lane = threadIdx.x & 31;
   if (flat >= rows) return;
   float m = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_lse[s * rows + flat]);
+  for (int s = lane; s < a.parts; s += 32) m = fmaxf(m, a.part_lse[s * rows + flat]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float base = m == -INFINITY ? 0.f : m;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) dense_combine_kernel(const DenseArgs
 #pragma unroll
   for (int c = 0; c < N; ++c) acc[c] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = 0; s < a.parts; ++s) {
     const float w = expf(a.part_lse[s * rows + flat] - base);
     const float* p = a.part_o + (s * rows + flat) * D + lane * N;
     total += w;

@@ -64,6 +64,8 @@ struct FwdBars {
   int abort;
 };
 
+static_assert(sizeof(FwdBars) <= 256, "the barriers fit their place");
+
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     dense_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
