@@ -79,11 +79,19 @@ def _keep(key, plan):
 
 
 class _Plan:
-    """A checked description of a call: the library's structures, the output shapes, scratch bytes."""
+    """A checked description of a call: the library's structures, the outputs it may have to make, scratch
+    bytes."""
 
-    def __init__(self, shape, device, nws=0, out_shapes=()):
-        self.shape, self.ref, self.device = shape, ctypes.byref(shape), device
-        self.nws, self.out_shapes = nws, out_shapes
+    def __init__(self, shape, device, dtype, nws=0, out_shapes=()):
+        self.shape, self.ref, self.device, self.dtype, self.nws = shape, ctypes.byref(shape), device, dtype, nws
+        self.outs = []
+        for size in out_shapes:
+            B, x, y, d = size
+            self.outs.append(((B, x, y, d), (x * y * d, y * d, d, 1)))
+
+    def make(self, i: int, stream) -> torch.Tensor:
+        """Output i, dense (the quickest of torch's ways to allocate a tensor)."""
+        return _made(torch.empty_strided(*self.outs[i], dtype=self.dtype, device=self.device), stream)
 
 
 _HERE = contextlib.nullcontext()
@@ -192,7 +200,7 @@ def _qk_plan(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps, ou
         shp.dq, shp.dk = strides(grads, ("dq", "dk"), (q.shape, k.shape), True)
         if q_weight is not None:
             nws = int(load().fvattn_qk_norm_rope_workspace_bytes(ctypes.byref(shp)))
-    return _keep(key, _Plan(shp, q.device, nws, shapes))
+    return _keep(key, _Plan(shp, q.device, q.dtype, nws, shapes if grads is None else (q.shape, k.shape)))
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
@@ -213,13 +221,13 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     plan = _qk_plan(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps, (q_out, k_out), None, status)
     handle = _handle(plan.device, stream)
     if q_out is None:
-        q_out = _made(torch.empty(plan.out_shapes[0], dtype=q.dtype, device=plan.device), stream)
+        q_out = plan.make(0, stream)
     if k_out is None:
-        k_out = _made(torch.empty(plan.out_shapes[1], dtype=q.dtype, device=plan.device), stream)
+        k_out = plan.make(1, stream)
     with _current(plan.device):
-        check(load().fvattn_qk_norm_rope(q.data_ptr(), k.data_ptr(), plan.ref, _ptr(q_weight), _ptr(k_weight), _ptr(cos),
-                                         _ptr(sin), _ptr(positions), q_out.data_ptr(), k_out.data_ptr(), _ptr(status),
-                                         handle), "fvattn_qk_norm_rope")
+        check(load().fvattn_qk_norm_rope(q.data_ptr(), k.data_ptr(), plan.ref, _ptr(q_weight), _ptr(k_weight),
+                                         _ptr(cos), _ptr(sin), _ptr(positions), q_out.data_ptr(), k_out.data_ptr(),
+                                         _ptr(status), handle), "fvattn_qk_norm_rope")
     return q_out, k_out
 
 
@@ -236,9 +244,9 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     plan = _qk_plan(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps, (dq_out, dk_out), (dq, dk), status)
     handle = _handle(plan.device, stream)
     if dq is None:
-        dq = _made(torch.empty(q.shape, dtype=q.dtype, device=plan.device), stream)
+        dq = plan.make(0, stream)
     if dk is None:
-        dk = _made(torch.empty(k.shape, dtype=q.dtype, device=plan.device), stream)
+        dk = plan.make(1, stream)
     dwq = dwk = None
     if q_weight is not None:
         dwq = _made(torch.empty(q.shape[3], dtype=torch.float32, device=plan.device), stream)
@@ -316,8 +324,8 @@ def _dense_shape(q, k, v, cfg: AttnConfig, scale: float) -> _lib.DenseShape:
 def _dense_plan(q, k, v, cfg: AttnConfig, scale, out, rest, lse, status, grads) -> _Plan:
     """grads: (dout, dq, dk, dv) of the gradients' call, None in the other."""
     key = ("dense", _meta(q), _meta(k), _meta(v), _meta(out), _meta(rest), _meta(lse), _meta(status), float(scale),
-           float(cfg.softcap), bool(cfg.causal), _meta(cfg.slopes), _meta(cfg.q_start), _meta(cfg.prefix_len), _meta(cfg.kv_len),
-           _meta(cfg.doc_q), _meta(cfg.doc_k), None if grads is None else tuple(map(_meta, grads)))
+           float(cfg.softcap), bool(cfg.causal), _meta(cfg.slopes), _meta(cfg.q_start), _meta(cfg.prefix_len),
+           _meta(cfg.kv_len), _meta(cfg.doc_q), _meta(cfg.doc_k), None if grads is None else tuple(map(_meta, grads)))
     plan = _plans.get(key)
     if plan is not None:
         return plan
@@ -349,8 +357,9 @@ def _dense_plan(q, k, v, cfg: AttnConfig, scale, out, rest, lse, status, grads) 
             setattr(shp, name, strides(t, name, like))
         nws = int(lib.fvattn_dense_attn_bwd_workspace_bytes(ctypes.byref(shp), mask))
     if nws == _lib.SIZE_ERROR:
-        return _Plan(shp, q.device)            # the call that follows says what is wrong
-    return _keep(key, _Plan(shp, q.device, nws))
+        # the call that follows says what is wrong
+        return _Plan(shp, q.device, q.dtype, 0, (q.shape, k.shape, v.shape))
+    return _keep(key, _Plan(shp, q.device, q.dtype, nws, (q.shape, k.shape, v.shape)))
 
 
 def dense_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cfg: Optional[AttnConfig] = None, *,
@@ -369,7 +378,7 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cfg: Optional[
     plan = _dense_plan(q, k, v, cfg, scale, out, rest, lse, status, None)
     handle = _handle(plan.device, stream)
     if out is None:
-        out = _made(torch.empty(q.shape, dtype=q.dtype, device=plan.device), stream)
+        out = plan.make(0, stream)
     ws = _scratch(plan, workspace, stream)
     with _current(plan.device):
         check(load().fvattn_dense_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()),
@@ -390,12 +399,13 @@ def dense_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     cfg = cfg or AttnConfig()
     plan = _dense_plan(q, k, v, cfg, scale, out, rest, lse, status, (dout, dq, dk, dv))
     handle = _handle(plan.device, stream)
-    dq, dk, dv = (_made(torch.empty(t.shape, dtype=q.dtype, device=plan.device), stream) if g is None else g
-                  for g, t in ((dq, q), (dk, k), (dv, v)))
+    dq = plan.make(0, stream) if dq is None else dq
+    dk = plan.make(1, stream) if dk is None else dk
+    dv = plan.make(2, stream) if dv is None else dv
     ws = _scratch(plan, workspace, stream)
     with _current(plan.device):
         check(load().fvattn_dense_attn_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                           _ptr(rest), lse.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()), dq.data_ptr(),
-                                           dk.data_ptr(), dv.data_ptr(), _ptr(ws), plan.nws, _ptr(status), handle),
-              "fvattn_dense_attn_bwd")
+                                           _ptr(rest), lse.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()),
+                                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), plan.nws,
+                                           _ptr(status), handle), "fvattn_dense_attn_bwd")
     return dq, dk, dv

@@ -43,7 +43,10 @@ constexpr int kT = 128;               // rows and keys of a tile
 // even for a barrier that is complete, and the products of a step take nearly as long to issue as to
 // run: one warp for all of them let the tensor cores run dry at each wait.
 constexpr int kWarps = 20;
-constexpr int kMmaS = 1, kMmaOut = 18, kMmaDp = 19;
+constexpr int kLoader = 16, kMmaS = 17, kMmaOut = 18, kMmaDp = 19;
+// Registers: of the 96 per thread at the launch the last four warps give up 56, the sixteen take 8 more
+// (128 x 40 + 512 x 104 = 58,368 of the launch's 61,440).
+constexpr int kRegsWork = 104, kRegsOther = 40;
 constexpr int kWork = 16;
 constexpr int kCols = kT * 4 / kWork; // columns of a score tile per thread
 constexpr int kThreads = kWarps * 32;
@@ -130,7 +133,7 @@ struct DkvBars {
 
 static_assert(sizeof(DkvBars) <= 512, "the barriers fit their place");
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool DOCS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -146,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tile_of(order, blockIdx.x, x, bh);        // the first keys are seen by the most rows under an order
   const int b = bh / a.Hkv, h = bh - b * a.Hkv, j0 = x * kT;
   const DenseSeq seq = dense_seq(a, b);
-  const int32_t* doc_q = a.mask.doc_q != nullptr ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
-  const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+  const int32_t* doc_q = DOCS ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
+  const int32_t* doc_k = DOCS ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
   const int tiles = (a.Sq + qpt - 1) / qpt;
 
   if (threadIdx.x == 0) {
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bars->doc_pad = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == kMmaS) {
     tc::tmem_alloc(&bars->tmem_base, 512);
     tc::tmem_relinquish();
   }
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (doc_k != nullptr) {
+  if (DOCS) {
     if (threadIdx.x < kT && j0 + threadIdx.x < a.Sk) {
       const int doc = doc_k[j0 + threadIdx.x];
       if (doc >= 0) {
@@ -208,155 +211,159 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (a.causal && j0 >= seq.prefix) {
     first = max(0, min(j0 - seq.q0, a.Sq)) / qpt;      // query i sees key j0 when q0 + i >= j0
   }
-  const int2* tile_docs = doc_q != nullptr ? a.doc_blocks_q + (int64_t)b * tiles : nullptr;
-  BlockWalk walk(tile_docs, first, tiles, bars->doc_lo, bars->doc_hi);
+  const int2* tile_docs = DOCS ? a.doc_blocks_q + (int64_t)b * tiles : nullptr;
+  BlockWalk<DOCS> walk(tile_docs, first, tiles, bars->doc_lo, bars->doc_hi);
   const uint32_t n = (uint32_t)walk.count(lane);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loader
-    bool kv_armed = false;
-    if (lane == 0 && n > 0) {
-      tc::mbar_expect_tx(&bars->kv_full, 2 * L::kKeyTile);
-      kv_armed = true;
-      for (int c = 0; c < D / 64; ++c) {
-        tc::tma_load_4d(smem + L::kOffK + c * L::kKeyChunk, &tmK, &bars->kv_full, c * 64, j0, h, b);
-        tc::tma_load_4d(smem + L::kOffV + c * L::kKeyChunk, &tmV, &bars->kv_full, c * 64, j0, h, b);
+  if (warp >= kWork) {
+    tc::regs_down<kRegsOther>();
+    if (warp == kLoader) {
+      // ------------------------------------------------------------ loader
+      bool kv_armed = false;
+      if (lane == 0 && n > 0) {
+        tc::mbar_expect_tx(&bars->kv_full, 2 * L::kKeyTile);
+        kv_armed = true;
+        for (int c = 0; c < D / 64; ++c) {
+          tc::tma_load_4d(smem + L::kOffK + c * L::kKeyChunk, &tmK, &bars->kv_full, c * 64, j0, h, b);
+          tc::tma_load_4d(smem + L::kOffV + c * L::kKeyChunk, &tmV, &bars->kv_full, c * 64, j0, h, b);
+        }
       }
-    }
-    const uint32_t bytes = (uint32_t)(qpt * a.G) * 128 * (D / 64);
-    uint32_t g = 0, q_armed = 0, g_armed = 0;      // steps whose copies were issued
-    // One tensor's rows of a step into their stage.
-    auto load = [&](const CUtensorMap& map, const void* base, const fvattn_strides& st, uint64_t* full, uint64_t* empty,
-                    uint32_t empty_parity, unsigned char* dst, int i0, bool pad) -> bool {
-      if (!warp_wait(empty, empty_parity, abort)) return false;
-      if (pad) {
-        // padding queries may hold anything: copied by hand, with zeros for them
-        copy_rows<D, kR>(dst, static_cast<const __nv_bfloat16*>(base), st, a, b, h, i0, qpt, doc_q, lane, 32);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(full);
-      } else if (lane == 0) {
-        tc::mbar_expect_tx(full, bytes);
-        for (int c = 0; c < D / 64; ++c) tc::tma_load_5d(dst + c * L::kRowChunk, &map, full, c * 64, 0, i0, h, b);
-      }
-      return true;
-    };
-    bool ok = true;
-    for (int t; ok && (t = walk.next(lane)) >= 0; ++g) {
-      const uint32_t sq = g % kStagesQ, sg = g % kStagesG;
-      const bool pad = tile_docs != nullptr && tile_docs[t].x < 0;
-      ok = load(tmQ, a.q, a.qs, &bars->q_full[sq], &bars->q_empty[sq], ((g / kStagesQ) & 1) ^ 1,
-                smem + L::kOffQ + sq * L::kRowTile, t * qpt, pad);
-      if (ok) q_armed = g + 1;
-      ok = ok && load(tmG, a.dout, a.dos, &bars->g_full[sg], &bars->g_empty[sg], ((g / kStagesG) & 1) ^ 1,
-                      smem + L::kOffG + sg * L::kRowTile, t * qpt, pad);
-      if (ok) g_armed = g + 1;
-    }
-    if (!ok) fail(&bars->abort, 3);
-    if (lane == 0) {
-      // no copy may still be writing shared memory when the CTA leaves: the last of each stage
-      if (kv_armed) tc::mbar_wait_drain(&bars->kv_full, 0, kWaitLimit);
-      for (uint32_t k = q_armed > kStagesQ ? q_armed - kStagesQ : 0; k < q_armed; ++k)
-        tc::mbar_wait_drain(&bars->q_full[k % kStagesQ], (k / kStagesQ) & 1, kWaitLimit);
-      for (uint32_t k = g_armed > kStagesG ? g_armed - kStagesG : 0; k < g_armed; ++k)
-        tc::mbar_wait_drain(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, kWaitLimit);
-    }
-  } else if (warp == kMmaS || warp == kMmaOut || warp == kMmaDp) {
-    // ------------------------------------------------------------ MMA issuers
-    // Each warp keeps step as a whole, so that what the products take is the same in all lanes; one lane
-    // issues.
-    if (n > 0) {
-      constexpr uint32_t idS = tc::idesc_bf16_f32(kT, kR, 0, 0), idD = tc::idesc_bf16_f32(kT, D, 0, 1);
-      constexpr uint32_t kStage = L::kRowTile >> 4;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
-        ok = ok && warp_wait(bar, parity, abort);
-        if (!ok) fail(&bars->abort, code);
-        tc::fence_after_sync();
-        return ok;
-      };
-      // scores^T (K, Q) or dP^T (V, dout): [128 keys x 64 rows] over the dims, for every step
-      auto over_dims = [&](int key_off, int row_off, uint32_t stages, uint64_t* full, uint64_t* over, uint32_t col,
-                           uint64_t* done, int code) {
-        const uint64_t key_tile = tc::smem_desc_sw128(tc::smem_u32(smem + key_off), 16, 1024);
-        const uint64_t row_tile = tc::smem_desc_sw128(tc::smem_u32(smem + row_off), 16, 1024);
-        wait(&bars->kv_full, 0, code);
-        uint32_t st = 0, turn = 0;       // stage of the step and how often it has come round
-        for (uint32_t k = 0; ok && k < n; ++k) {
-          const uint32_t p = k & 1;
-          // what the step before last left in the columns has been read
-          if (k >= 2 && !wait(&over[p], ((k >> 1) & 1) ^ 1, code)) break;
-          if (!wait(&full[st], turn & 1, code + 10)) break;
-          if (tc::elect_one()) {
-            const uint64_t rd = row_tile + st * kStage;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc::mma_f16(tbase + col + p * kR, key_tile + (((kk >> 2) * L::kKeyChunk + (kk & 3) * 32) >> 4),
-                          rd + (((kk >> 2) * L::kRowChunk + (kk & 3) * 32) >> 4), idS, kk > 0);
-            tc::mma_commit(&done[p]);
-          }
+      const uint32_t bytes = (uint32_t)(qpt * a.G) * 128 * (D / 64);
+      uint32_t g = 0, q_armed = 0, g_armed = 0;      // steps whose copies were issued
+      // One tensor's rows of a step into their stage.
+      auto load = [&](const CUtensorMap& map, const void* base, const fvattn_strides& st, uint64_t* full, uint64_t* empty,
+                      uint32_t empty_parity, unsigned char* dst, int i0, bool pad) -> bool {
+        if (!warp_wait(empty, empty_parity, abort)) return false;
+        if (pad) {
+          // padding queries may hold anything: copied by hand, with zeros for them
+          copy_rows<D, kR>(dst, static_cast<const __nv_bfloat16*>(base), st, a, b, h, i0, qpt, doc_q, lane, 32);
+          tc::fence_proxy_async_smem();
           __syncwarp();
-          if (++st == stages) {
-            st = 0;
-            ++turn;
-          }
+          if (lane == 0) tc::mbar_arrive(full);
+        } else if (lane == 0) {
+          tc::mbar_expect_tx(full, bytes);
+          for (int c = 0; c < D / 64; ++c) tc::tma_load_5d(dst + c * L::kRowChunk, &map, full, c * 64, 0, i0, h, b);
         }
+        return true;
       };
-      if (warp == kMmaS) {
-        over_dims(L::kOffK, L::kOffQ, kStagesQ, bars->q_full, bars->dv_done, L::kColS, bars->s_full, 5);
-      } else if (warp == kMmaDp) {
-        over_dims(L::kOffV, L::kOffG, kStagesG, bars->g_full, bars->dk_done, L::kColDp, bars->dp_full, 6);
-      } else {
-        const uint64_t qt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffQ), L::kRowChunk, 1024);
-        const uint64_t gt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffG), L::kRowChunk, 1024);
-        // dV or dK += [128 keys x 64 rows] (bf16 in TMEM, every kCols rows over their fp32 values) x [rows x D]
-        auto over_rows = [&](uint32_t d_tmem, uint32_t w, uint64_t row_tile, uint32_t add) {
-#pragma unroll
-          for (int kk = 0; kk < kR / 16; ++kk)
-            tc::mma_f16_tmem_a(d_tmem, w + (kk >> 1) * kCols + (kk & 1) * 8, row_tile + ((kk * 16 * 128) >> 4), idD,
-                               kk > 0 ? 1u : add);
+      bool ok = true;
+      for (int t; ok && (t = walk.next(lane)) >= 0; ++g) {
+        const uint32_t sq = g % kStagesQ, sg = g % kStagesG;
+        const bool pad = DOCS && walk.doc().x < 0;
+        ok = load(tmQ, a.q, a.qs, &bars->q_full[sq], &bars->q_empty[sq], ((g / kStagesQ) & 1) ^ 1,
+                  smem + L::kOffQ + sq * L::kRowTile, t * qpt, pad);
+        if (ok) q_armed = g + 1;
+        ok = ok && load(tmG, a.dout, a.dos, &bars->g_full[sg], &bars->g_empty[sg], ((g / kStagesG) & 1) ^ 1,
+                        smem + L::kOffG + sg * L::kRowTile, t * qpt, pad);
+        if (ok) g_armed = g + 1;
+      }
+      if (!ok) fail(&bars->abort, 3);
+      if (lane == 0) {
+        // no copy may still be writing shared memory when the CTA leaves: the last of each stage
+        if (kv_armed) tc::mbar_wait_drain(&bars->kv_full, 0, kWaitLimit);
+        for (uint32_t k = q_armed > kStagesQ ? q_armed - kStagesQ : 0; k < q_armed; ++k)
+          tc::mbar_wait_drain(&bars->q_full[k % kStagesQ], (k / kStagesQ) & 1, kWaitLimit);
+        for (uint32_t k = g_armed > kStagesG ? g_armed - kStagesG : 0; k < g_armed; ++k)
+          tc::mbar_wait_drain(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, kWaitLimit);
+      }
+    } else {
+      // ------------------------------------------------------------ MMA issuers
+      // Each warp keeps step as a whole, so that what the products take is the same in all lanes; one lane
+      // issues.
+      if (n > 0) {
+        constexpr uint32_t idS = tc::idesc_bf16_f32(kT, kR, 0, 0), idD = tc::idesc_bf16_f32(kT, D, 0, 1);
+        constexpr uint32_t kStage = L::kRowTile >> 4;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+          ok = ok && warp_wait(bar, parity, abort);
+          if (!ok) fail(&bars->abort, code);
+          tc::fence_after_sync();
+          return ok;
         };
-        for (uint32_t k = 0; ok && k <= n; ++k) {
-          const uint32_t p = k & 1;
-          if (k < n) {
-            // P(k) says that Q(k) has landed, not that dout(k) has
-            if (!wait(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, 7)) break;
-            if (!wait(&bars->p_full[p], (k >> 1) & 1, 8)) break;
+        // scores^T (K, Q) or dP^T (V, dout): [128 keys x 64 rows] over the dims, for every step
+        auto over_dims = [&](int key_off, int row_off, uint32_t stages, uint64_t* full, uint64_t* over, uint32_t col,
+                             uint64_t* done, int code) {
+          const uint64_t key_tile = tc::smem_desc_sw128(tc::smem_u32(smem + key_off), 16, 1024);
+          const uint64_t row_tile = tc::smem_desc_sw128(tc::smem_u32(smem + row_off), 16, 1024);
+          wait(&bars->kv_full, 0, code);
+          uint32_t st = 0, turn = 0;       // stage of the step and how often it has come round
+          for (uint32_t k = 0; ok && k < n; ++k) {
+            const uint32_t p = k & 1;
+            // what the step before last left in the columns has been read
+            if (k >= 2 && !wait(&over[p], ((k >> 1) & 1) ^ 1, code)) break;
+            if (!wait(&full[st], turn & 1, code + 10)) break;
             if (tc::elect_one()) {
-              over_rows(tbase + L::kColV, tbase + L::kColS + p * kR, gt + (k % kStagesG) * kStage, k > 0);
-              tc::mma_commit(&bars->dv_done[p]);
+              const uint64_t rd = row_tile + st * kStage;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_f16(tbase + col + p * kR, key_tile + (((kk >> 2) * L::kKeyChunk + (kk & 3) * 32) >> 4),
+                            rd + (((kk >> 2) * L::kRowChunk + (kk & 3) * 32) >> 4), idS, kk > 0);
+              tc::mma_commit(&done[p]);
             }
             __syncwarp();
+            if (++st == stages) {
+              st = 0;
+              ++turn;
+            }
           }
-          if (k > 0) {
-            const uint32_t e = k - 1;
-            if (!wait(&bars->ds_full[p ^ 1], (e >> 1) & 1, 9)) break;
-            if (tc::elect_one()) {
-              over_rows(tbase + L::kColK, tbase + L::kColDp + (p ^ 1) * kR, qt + (e % kStagesQ) * kStage, e > 0);
-              tc::mma_commit(&bars->dk_done[p ^ 1]);
-              // dS(e) was made from S(e) and dP(e), so with dK(e) all four products of the step are done
-              tc::mma_commit(&bars->q_empty[e % kStagesQ]);
-              tc::mma_commit(&bars->g_empty[e % kStagesG]);
+        };
+        if (warp == kMmaS) {
+          over_dims(L::kOffK, L::kOffQ, kStagesQ, bars->q_full, bars->dv_done, L::kColS, bars->s_full, 5);
+        } else if (warp == kMmaDp) {
+          over_dims(L::kOffV, L::kOffG, kStagesG, bars->g_full, bars->dk_done, L::kColDp, bars->dp_full, 6);
+        } else {
+          const uint64_t qt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffQ), L::kRowChunk, 1024);
+          const uint64_t gt = tc::smem_desc_sw128(tc::smem_u32(smem + L::kOffG), L::kRowChunk, 1024);
+          // dV or dK += [128 keys x 64 rows] (bf16 in TMEM, every kCols rows over their fp32 values) x [rows x D]
+          auto over_rows = [&](uint32_t d_tmem, uint32_t w, uint64_t row_tile, uint32_t add) {
+#pragma unroll
+            for (int kk = 0; kk < kR / 16; ++kk)
+              tc::mma_f16_tmem_a(d_tmem, w + (kk >> 1) * kCols + (kk & 1) * 8, row_tile + ((kk * 16 * 128) >> 4), idD,
+                                 kk > 0 ? 1u : add);
+          };
+          for (uint32_t k = 0; ok && k <= n; ++k) {
+            const uint32_t p = k & 1;
+            if (k < n) {
+              // P(k) says that Q(k) has landed, not that dout(k) has
+              if (!wait(&bars->g_full[k % kStagesG], (k / kStagesG) & 1, 7)) break;
+              if (!wait(&bars->p_full[p], (k >> 1) & 1, 8)) break;
+              if (tc::elect_one()) {
+                over_rows(tbase + L::kColV, tbase + L::kColS + p * kR, gt + (k % kStagesG) * kStage, k > 0);
+                tc::mma_commit(&bars->dv_done[p]);
+              }
+              __syncwarp();
             }
-            __syncwarp();
+            if (k > 0) {
+              const uint32_t e = k - 1;
+              if (!wait(&bars->ds_full[p ^ 1], (e >> 1) & 1, 9)) break;
+              if (tc::elect_one()) {
+                over_rows(tbase + L::kColK, tbase + L::kColDp + (p ^ 1) * kR, qt + (e % kStagesQ) * kStage, e > 0);
+                tc::mma_commit(&bars->dk_done[p ^ 1]);
+                // dS(e) was made from S(e) and dP(e), so with dK(e) all four products of the step are done
+                tc::mma_commit(&bars->q_empty[e % kStagesQ]);
+                tc::mma_commit(&bars->g_empty[e % kStagesG]);
+              }
+              __syncwarp();
+            }
           }
         }
+        // on every path: the products issued so far are done before TMEM is read or released
+        if (tc::elect_one()) tc::mma_commit(&bars->drain);
+        __syncwarp();
+        if (lane == 0) tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+        __syncwarp();
       }
-      // on every path: the products issued so far are done before TMEM is read or released
-      if (tc::elect_one()) tc::mma_commit(&bars->drain);
-      __syncwarp();
-      if (lane == 0) tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
-      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ elementwise
+    tc::regs_up<kRegsWork>();
     // TMEM lane quarter, group (steps of its parity), columns of the step
-    const int q = warp & 3, group = (warp - 2) >> 3, col0 = (((warp - 2) >> 2) & 1) * kCols;
+    const int q = warp & 3, group = warp >> 3, col0 = ((warp >> 2) & 1) * kCols;
     const int r = q * 32 + lane, j = j0 + r;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t colS = tbase + lanes + L::kColS + group * kR + col0, colP = tbase + lanes + L::kColDp + group * kR + col0;
     RowStats* stats = reinterpret_cast<RowStats*>(smem + L::kOffStats) + 2 * group;
-    const int my_doc = doc_k != nullptr && j < a.Sk ? doc_k[j] : 0;
+    const int my_doc = DOCS && j < a.Sk ? doc_k[j] : 0;
     const bool key_ok = j < seq.kv && my_doc >= 0;
     const float in = CAP ? a.scale / a.cap : 0.f, factor = (CAP ? a.cap : a.scale) * kLog2e, fr = (float)r;
     const uint64_t factor2 = f2(factor, factor);
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // The row statistics of a step: these threads hold one value each of the group's next step in flight,
     // as loaded (nothing waits for it), and write it at the start of its turn.
-    const int tid = threadIdx.x - 64 - group * (kWork / 2) * 32;
+    const int tid = threadIdx.x - group * (kWork / 2) * 32;
     const int part = tid / kR, sr = tid % kR, si = sr / a.G, sg = sr - si * a.G;
     float ahead = 0.f;       // lse, delta, document or slope of row sr
     int ahead_limit = 0;     // its limit or position
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (part == 1) ahead = a.delta[flat];
       if (part == 2) {
         ahead_limit = dense_limit(seq, a.causal, i);
-        if (doc_q != nullptr) ahead = __int_as_float(doc_q[i]);
+        if (DOCS) ahead = __int_as_float(doc_q[i]);
       }
       if (BIAS && part == 3) {
         ahead_limit = seq.q0 + i;
@@ -460,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int t = walk.next(lane);
     if (group == 1) t = walk.next(lane);
+    int2 docs = t >= 0 ? walk.doc() : make_int2(0, 0);       // of step t
     if (t >= 0) fetch(t);
     for (uint32_t turn = 0; t >= 0; ++turn) {
       RowStats& st = stats[turn & 1];
@@ -468,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_sync(1 + group, kWork / 2 * 32);      // after an abort too: every warp takes all its turns
       walk.next(lane);                            // the other group's
       const int next = walk.next(lane);
+      const int2 next_docs = next >= 0 ? walk.doc() : make_int2(0, 0);
       if (next >= 0) fetch(next);
       see = (uint32_t)(low64(min(qpt, a.Sq - i0) * a.G - col0) & 0xffffffffull);
       // limits never fall along the rows: the first query's is the least
@@ -480,9 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         see &= below;
       }
-      if (tile_docs != nullptr) {
-        const int2 v = tile_docs[t];
-        if (!one_doc || !doc_uniform(v) || v.y != bars->doc_lo) {
+      if (DOCS) {
+        if (!one_doc || !doc_uniform(docs) || docs.y != bars->doc_lo) {
           see &= (uint32_t)same_document(st.doc[col0 + lane], -1, my_doc);
           if (!key_ok) see = 0u;
         }
@@ -513,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&bars->ds_full[group]);
       }
       t = next;
+      docs = next_docs;
     }
     // ------------------------------------------------------------ results: one group writes dV, the other dK
     if (n > 0 && ok) {
@@ -520,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
     }
     const bool broken = __any_sync(0xffffffffu, *abort != 0);
-    const int part_d = ((warp - 2) >> 2) & 1;
+    const int part_d = (warp >> 2) & 1;
     const float by = broken ? __int_as_float(0x7fffffff) : group == 0 ? 1.f : a.scale;
     const fvattn_strides& ss = group == 0 ? a.dvs : a.dks;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(group == 0 ? a.dv : a.dk) + (int64_t)b * ss.b + (int64_t)h * ss.h +
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(tbase, 512);
+  if (warp == kMmaS) tc::tmem_dealloc(tbase, 512);
   if (threadIdx.x == 0 && bars->abort && a.status != nullptr)
     report_error(a.status, FVATTN_ERR_TIMEOUT, 300 + bars->abort);
 }
@@ -574,7 +583,7 @@ struct DqBars {
 
 static_assert(sizeof(DqBars) <= 256, "the barriers fit their place");
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool DOCS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -592,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t = order.tiles - 1 - x, b = bh / a.Hkv, h = bh - b * a.Hkv;      // the longest tiles first
   const int i0 = t * qpt, i1 = min(i0 + qpt, a.Sq);
   const DenseSeq seq = dense_seq(a, b);
-  const int32_t* doc_q = a.mask.doc_q != nullptr ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
-  const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+  const int32_t* doc_q = DOCS ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
+  const int32_t* doc_k = DOCS ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
   const int blocks = (a.Sk + kT - 1) / kT;
 
   if (threadIdx.x == 0) {
@@ -616,14 +625,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bars->doc_hi = -1;
     tc::fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == kMmaS) {
     tc::tmem_alloc(&bars->tmem_base, 512);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (doc_q != nullptr) {
+  if (DOCS) {
     for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
       const int doc = doc_q[i];
       if (doc >= 0) {
@@ -635,130 +644,134 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   const int key1 = dense_limit(seq, a.causal, i1 - 1);
-  BlockWalk walk(a.doc_blocks_k != nullptr ? a.doc_blocks_k + (int64_t)b * blocks : nullptr, 0, (key1 + kT - 1) / kT,
+  BlockWalk<DOCS> walk(DOCS ? a.doc_blocks_k + (int64_t)b * blocks : nullptr, 0, (key1 + kT - 1) / kT,
                  bars->doc_lo, bars->doc_hi);
   const uint32_t n = (uint32_t)walk.count(lane);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loader
-    uint32_t g = 0, k_armed = 0, v_armed = 0;      // steps whose copies were issued
-    bool q_armed = false, ok = true;
-    for (int j; ok && (j = walk.next(lane)) >= 0; ++g) {
-      const uint32_t sk = g % 3, sv = g & 1;
-      unsigned char* dk = smem + L::kOffK + sk * L::kTile;
-      if (g == 0) {
-        if (lane == 0) {
-          tc::mbar_expect_tx(&bars->q_full, 2 * (uint32_t)(qpt * a.G) * 128 * (D / 64));
-          for (int c = 0; c < D / 64; ++c) {
-            tc::tma_load_5d(smem + L::kOffQ + c * L::kChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
-            tc::tma_load_5d(smem + L::kOffG + c * L::kChunk, &tmG, &bars->q_full, c * 64, 0, i0, h, b);
-          }
-        }
-        q_armed = true;
-      }
-      ok = warp_wait(&bars->k_empty[sk], ((g / 3) & 1) ^ 1, abort);
-      if (!ok) break;
-      // keys that do not exist: zeros, whatever their memory holds (0 * NaN would reach dQ)
-      const bool dirty = (seq.kv < a.Sk && (j + 1) * kT > seq.kv) || (doc_k != nullptr && walk.docs[j].x < 0);
-      if (dirty) {
-        copy_keys<D>(dk, static_cast<const __nv_bfloat16*>(a.k) + (int64_t)b * a.ks.b + (int64_t)h * a.ks.h, a.ks.s, j * kT,
-                     kT, seq.kv, doc_k, lane, 32);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->k_full[sk]);
-      } else if (lane == 0) {
-        tc::mbar_expect_tx(&bars->k_full[sk], L::kTile);
-        for (int c = 0; c < D / 64; ++c)
-          tc::tma_load_4d(dk + c * L::kChunk, &tmK, &bars->k_full[sk], c * 64, j * kT, h, b);
-      }
-      k_armed = g + 1;
-      ok = warp_wait(&bars->v_empty[sv], ((g >> 1) & 1) ^ 1, abort);
-      if (!ok) break;
-      if (lane == 0) {
-        tc::mbar_expect_tx(&bars->v_full[sv], L::kTile);
-        for (int c = 0; c < D / 64; ++c)
-          tc::tma_load_4d(smem + L::kOffV + sv * L::kTile + c * L::kChunk, &tmV, &bars->v_full[sv], c * 64, j * kT, h, b);
-      }
-      v_armed = g + 1;
-    }
-    if (!ok) fail(&bars->abort, 3);
-    if (lane == 0) {
-      // no copy may still be writing shared memory when the CTA leaves: the last of each stage
-      if (q_armed) tc::mbar_wait_drain(&bars->q_full, 0, kWaitLimit);
-      for (uint32_t k = k_armed > 3 ? k_armed - 3 : 0; k < k_armed; ++k)
-        tc::mbar_wait_drain(&bars->k_full[k % 3], (k / 3) & 1, kWaitLimit);
-      for (uint32_t k = v_armed > 2 ? v_armed - 2 : 0; k < v_armed; ++k)
-        tc::mbar_wait_drain(&bars->v_full[k & 1], (k >> 1) & 1, kWaitLimit);
-    }
-  } else if (warp == kMmaS || warp == kMmaOut || warp == kMmaDp) {
-    // ------------------------------------------------------------ MMA issuers
-    // Each warp keeps step as a whole, so that what the products take is the same in all lanes; one lane
-    // issues. One warp makes dP and dQ, in this order: dS(g+1) waits for dP(g+1).
-    if (n > 0 && warp != kMmaDp) {
-      constexpr uint32_t kStage = L::kTile >> 4;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
-        ok = ok && warp_wait(bar, parity, abort);
-        if (!ok) fail(&bars->abort, code);
-        tc::fence_after_sync();
-        return ok;
-      };
-      wait(&bars->q_full, 0, 7);
-      uint32_t st = 0, turn = 0;       // K's stage of the step and how often it has come round
-      auto advance = [&] {
-        if (++st == L::kStagesK) {
-          st = 0;
-          ++turn;
-        }
-      };
-      if (warp == kMmaS) {
-        const uint64_t qa = desc_dims(tc::smem_u32(smem + L::kOffQ)), kd = desc_dims(tc::smem_u32(smem + L::kOffK));
-        for (uint32_t g = 0; ok && g < n; ++g) {
-          // dS of the step before last has been read
-          if (g >= 2 && !wait(&bars->dq_done[g & 1], ((g >> 1) & 1) ^ 1, 4)) break;
-          if (!wait(&bars->k_full[st], turn & 1, 5)) break;
-          if (tc::elect_one()) {
-            mma_dims<D>(tbase + (g & 1 ? kColB : kColA), qa, kd + st * kStage);
-            tc::mma_commit(&bars->s_full[g & 1]);
-          }
-          __syncwarp();
-          advance();
-        }
-      } else {
-        const uint64_t ga = desc_dims(tc::smem_u32(smem + L::kOffG)), vd = desc_dims(tc::smem_u32(smem + L::kOffV));
-        const uint64_t kt = desc_tokens(tc::smem_u32(smem + L::kOffK));
-        for (uint32_t g = 0; ok && g <= n; ++g) {
-          if (g < n && !wait(&bars->v_full[g & 1], (g >> 1) & 1, 6)) break;
-          // dP(g) may overwrite dP(g-1) once dS(g-1) has been made from it
-          if (g > 0 && !wait(&bars->ds_full, (g - 1) & 1, 8)) break;
-          if (g < n) {
-            if (tc::elect_one()) {
-              mma_dims<D>(tbase + L::kColDp, ga, vd + (g & 1) * kStage);
-              tc::mma_commit(&bars->dp_full);
-              tc::mma_commit(&bars->v_empty[g & 1]);
+  if (warp >= kWork) {
+    tc::regs_down<kRegsOther>();
+    if (warp == kLoader) {
+      // ------------------------------------------------------------ loader
+      uint32_t g = 0, k_armed = 0, v_armed = 0;      // steps whose copies were issued
+      bool q_armed = false, ok = true;
+      for (int j; ok && (j = walk.next(lane)) >= 0; ++g) {
+        const uint32_t sk = g % 3, sv = g & 1;
+        unsigned char* dk = smem + L::kOffK + sk * L::kTile;
+        if (g == 0) {
+          if (lane == 0) {
+            tc::mbar_expect_tx(&bars->q_full, 2 * (uint32_t)(qpt * a.G) * 128 * (D / 64));
+            for (int c = 0; c < D / 64; ++c) {
+              tc::tma_load_5d(smem + L::kOffQ + c * L::kChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
+              tc::tma_load_5d(smem + L::kOffG + c * L::kChunk, &tmG, &bars->q_full, c * 64, 0, i0, h, b);
             }
-            __syncwarp();
           }
-          if (g > 0) {
-            const uint32_t e = g - 1;
+          q_armed = true;
+        }
+        ok = warp_wait(&bars->k_empty[sk], ((g / 3) & 1) ^ 1, abort);
+        if (!ok) break;
+        // keys that do not exist: zeros, whatever their memory holds (0 * NaN would reach dQ)
+        const bool dirty = (seq.kv < a.Sk && (j + 1) * kT > seq.kv) || (DOCS && walk.doc().x < 0);
+        if (dirty) {
+          copy_keys<D>(dk, static_cast<const __nv_bfloat16*>(a.k) + (int64_t)b * a.ks.b + (int64_t)h * a.ks.h, a.ks.s, j * kT,
+                       kT, seq.kv, doc_k, lane, 32);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars->k_full[sk]);
+        } else if (lane == 0) {
+          tc::mbar_expect_tx(&bars->k_full[sk], L::kTile);
+          for (int c = 0; c < D / 64; ++c)
+            tc::tma_load_4d(dk + c * L::kChunk, &tmK, &bars->k_full[sk], c * 64, j * kT, h, b);
+        }
+        k_armed = g + 1;
+        ok = warp_wait(&bars->v_empty[sv], ((g >> 1) & 1) ^ 1, abort);
+        if (!ok) break;
+        if (lane == 0) {
+          tc::mbar_expect_tx(&bars->v_full[sv], L::kTile);
+          for (int c = 0; c < D / 64; ++c)
+            tc::tma_load_4d(smem + L::kOffV + sv * L::kTile + c * L::kChunk, &tmV, &bars->v_full[sv], c * 64, j * kT, h, b);
+        }
+        v_armed = g + 1;
+      }
+      if (!ok) fail(&bars->abort, 3);
+      if (lane == 0) {
+        // no copy may still be writing shared memory when the CTA leaves: the last of each stage
+        if (q_armed) tc::mbar_wait_drain(&bars->q_full, 0, kWaitLimit);
+        for (uint32_t k = k_armed > 3 ? k_armed - 3 : 0; k < k_armed; ++k)
+          tc::mbar_wait_drain(&bars->k_full[k % 3], (k / 3) & 1, kWaitLimit);
+        for (uint32_t k = v_armed > 2 ? v_armed - 2 : 0; k < v_armed; ++k)
+          tc::mbar_wait_drain(&bars->v_full[k & 1], (k >> 1) & 1, kWaitLimit);
+      }
+    } else {
+      // ------------------------------------------------------------ MMA issuers
+      // Each warp keeps step as a whole, so that what the products take is the same in all lanes; one lane
+      // issues. One warp makes dP and dQ, in this order: dS(g+1) waits for dP(g+1).
+      if (n > 0 && warp != kMmaDp) {
+        constexpr uint32_t kStage = L::kTile >> 4;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+          ok = ok && warp_wait(bar, parity, abort);
+          if (!ok) fail(&bars->abort, code);
+          tc::fence_after_sync();
+          return ok;
+        };
+        wait(&bars->q_full, 0, 7);
+        uint32_t st = 0, turn = 0;       // K's stage of the step and how often it has come round
+        auto advance = [&] {
+          if (++st == L::kStagesK) {
+            st = 0;
+            ++turn;
+          }
+        };
+        if (warp == kMmaS) {
+          const uint64_t qa = desc_dims(tc::smem_u32(smem + L::kOffQ)), kd = desc_dims(tc::smem_u32(smem + L::kOffK));
+          for (uint32_t g = 0; ok && g < n; ++g) {
+            // dS of the step before last has been read
+            if (g >= 2 && !wait(&bars->dq_done[g & 1], ((g >> 1) & 1) ^ 1, 4)) break;
+            if (!wait(&bars->k_full[st], turn & 1, 5)) break;
             if (tc::elect_one()) {
-              mma_tokens<D>(tbase + L::kColQ, tbase + (e & 1 ? kColB : kColA), kt + st * kStage, e > 0);
-              tc::mma_commit(&bars->dq_done[e & 1]);
-              tc::mma_commit(&bars->k_empty[st]);
+              mma_dims<D>(tbase + (g & 1 ? kColB : kColA), qa, kd + st * kStage);
+              tc::mma_commit(&bars->s_full[g & 1]);
             }
             __syncwarp();
             advance();
           }
+        } else {
+          const uint64_t ga = desc_dims(tc::smem_u32(smem + L::kOffG)), vd = desc_dims(tc::smem_u32(smem + L::kOffV));
+          const uint64_t kt = desc_tokens(tc::smem_u32(smem + L::kOffK));
+          for (uint32_t g = 0; ok && g <= n; ++g) {
+            if (g < n && !wait(&bars->v_full[g & 1], (g >> 1) & 1, 6)) break;
+            // dP(g) may overwrite dP(g-1) once dS(g-1) has been made from it
+            if (g > 0 && !wait(&bars->ds_full, (g - 1) & 1, 8)) break;
+            if (g < n) {
+              if (tc::elect_one()) {
+                mma_dims<D>(tbase + L::kColDp, ga, vd + (g & 1) * kStage);
+                tc::mma_commit(&bars->dp_full);
+                tc::mma_commit(&bars->v_empty[g & 1]);
+              }
+              __syncwarp();
+            }
+            if (g > 0) {
+              const uint32_t e = g - 1;
+              if (tc::elect_one()) {
+                mma_tokens<D>(tbase + L::kColQ, tbase + (e & 1 ? kColB : kColA), kt + st * kStage, e > 0);
+                tc::mma_commit(&bars->dq_done[e & 1]);
+                tc::mma_commit(&bars->k_empty[st]);
+              }
+              __syncwarp();
+              advance();
+            }
+          }
         }
+        if (tc::elect_one()) tc::mma_commit(&bars->drain);
+        __syncwarp();
+        if (lane == 0) tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
+        __syncwarp();
       }
-      if (tc::elect_one()) tc::mma_commit(&bars->drain);
-      __syncwarp();
-      if (lane == 0) tc::mbar_wait_drain(&bars->drain, 0, kWaitLimit);
-      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ elementwise
-    const int q = warp & 3, cg = (warp - 2) >> 2, col0 = cg * kCols;      // TMEM lane quarter, keys of a tile
+    tc::regs_up<kRegsWork>();
+    const int q = warp & 3, cg = warp >> 2, col0 = cg * kCols;      // TMEM lane quarter, keys of a tile
     const int r = q * 32 + lane, i = i0 + r / a.G, hq = h * a.G + r % a.G;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const bool valid = r < qpt * a.G && i < a.Sq;
@@ -826,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j; (j = walk.next(lane)) >= 0; ++g) {
       const uint32_t colS = tbase + lanes + (g & 1 ? kColB : kColA) + col0;
       const int first = j * kT + col0;
-      see = (uint32_t)visible64(row, doc_k, doc_k != nullptr ? walk.docs[j] : make_int2(0, 0), first, a.Sk, lane);
+      see = (uint32_t)visible64<DOCS>(row, doc_k, walk.doc(), first, a.Sk, lane);
       const bool hidden = __any_sync(0xffffffffu, see != 0xffffffffu);
       if (!warp_wait(&bars->s_full[g & 1], (g >> 1) & 1, abort)) {
         fail(&bars->abort, 10);
@@ -871,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(tbase, 512);
+  if (warp == kMmaS) tc::tmem_dealloc(tbase, 512);
   if (threadIdx.x == 0 && bars->abort && a.status != nullptr)
     report_error(a.status, FVATTN_ERR_TIMEOUT, 400 + bars->abort);
 }
@@ -879,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // All of TMEM is one CTA's, so no second one may share the SM: it would wait for the first to leave.
 constexpr size_t kAloneBytes = 120 * 1024;
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool DOCS>
 cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   const int qpt = kTileRows / a.G;
   const int qpr = kR / a.G;
@@ -889,7 +902,7 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
       !make_map_keys(&mk, a.k, a.ks, a, kT) || !make_map_keys(&mv, a.v, a.vs, a, kT))
     return cudaErrorInvalidValue;
   {
-    auto* kernel = dense_dkv_tc_kernel<D, CAP, BIAS>;
+    auto* kernel = dense_dkv_tc_kernel<D, CAP, BIAS, DOCS>;
     const size_t smem = imax<size_t>(DkvLayout<D>::kBytes + 1024, kAloneBytes);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -899,7 +912,7 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  auto* kernel = dense_dq_tc_kernel<D, CAP, BIAS>;
+  auto* kernel = dense_dq_tc_kernel<D, CAP, BIAS, DOCS>;
   const size_t smem = imax<size_t>(DqLayout<D>::kBytes + 1024, kAloneBytes);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -909,11 +922,16 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <int D, bool DOCS>
+cudaError_t launch_docs(const DenseArgs& a, cudaStream_t st) {
+  const bool cap = a.cap > 0.f, bias = a.mask.slopes != nullptr;
+  if (cap) return bias ? launch<D, true, true, DOCS>(a, st) : launch<D, true, false, DOCS>(a, st);
+  return bias ? launch<D, false, true, DOCS>(a, st) : launch<D, false, false, DOCS>(a, st);
+}
+
 template <int D>
 cudaError_t launch_d(const DenseArgs& a, cudaStream_t st) {
-  const bool cap = a.cap > 0.f, bias = a.mask.slopes != nullptr;
-  if (cap) return bias ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
-  return bias ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
+  return a.mask.doc_k != nullptr ? launch_docs<D, true>(a, st) : launch_docs<D, false>(a, st);
 }
 
 }  // namespace

@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 }
 
 // grid: (splits, B * Hkv), clusters of `a.cluster` splits
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool DOCS>
 __global__ void __launch_bounds__(kThreads, 2)
     dense_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DenseArgs a) {
   using L = FewLayout<D>;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort = &bars->abort;
   const int split = blockIdx.x, bh = blockIdx.y, b = bh / a.Hkv, h = bh - b * a.Hkv;
   const DenseSeq seq = dense_seq(a, b);
-  const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+  const int32_t* doc_k = DOCS ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
   const int nrows = a.Sq * a.G;
   const int key0 = split * a.split_keys;
   const int key1 = (int)imin<int64_t>(dense_limit(seq, a.causal, a.Sq - 1), (int64_t)key0 + a.split_keys);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     bars->abort = 0;
     int lo = 0x7fffffff, hi = -1;
-    if (a.mask.doc_q != nullptr) {
+    if (DOCS) {
       for (int i = 0; i < a.Sq; ++i) {
         const int d = a.mask.doc_q[(int64_t)b * a.Sq + i];
         if (d >= 0) {
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc::fence_mbar_init();
   }
   __syncthreads();
-  const int2* docs = a.doc_blocks_k != nullptr ? a.doc_blocks_k + (int64_t)b * ((a.Sk + kBlock - 1) / kBlock) : nullptr;
-  BlockWalk walk(docs, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
+  const int2* docs = DOCS ? a.doc_blocks_k + (int64_t)b * ((a.Sk + kBlock - 1) / kBlock) : nullptr;
+  BlockWalk<DOCS> walk(docs, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
 
   // Thread (lane) of a warp with keys: rows r0 = lane / 4 and r0 + 8; columns 2 (lane % 4) and the next of
   // every eight.
@@ -189,11 +189,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t ka = tc::smem_u32(smem + s * L::kStage), va = tc::smem_u32(sv);
       const int first = j * kBlock + warp * 16;
       // keys that do not exist although their memory does: zeros, whatever it holds (0 * NaN would reach O)
-      const bool dirty = (seq.kv < a.Sk && (j + 1) * kBlock > seq.kv) || (docs != nullptr && docs[j].x < 0);
+      const bool dirty = (seq.kv < a.Sk && (j + 1) * kBlock > seq.kv) || (DOCS && walk.doc().x < 0);
       if (dirty) {
         for (int x = lane; x < 16 * (D / 8); x += 32) {
           const int r = x / (D / 8), key = first + r;
-          if (key >= seq.kv || (doc_k != nullptr && doc_k[key] < 0))
+          if (key >= seq.kv || (DOCS && doc_k[key] < 0))
             *reinterpret_cast<uint4*>(sv + tile_at(warp * 16 + r, x % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
         }
         tc::fence_proxy_async_smem();
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           float x = CAP ? tanh_any(sc[n][e] * in) : sc[n][e];
           x *= factor;
           if (BIAS) x = fmaf(-row[u].slope * kLog2e, (float)abs(row[u].pos - key), x);
-          const bool see = key < row[u].limit && (doc_k == nullptr || doc_k[key] == row[u].doc);
+          const bool see = key < row[u].limit && (!DOCS || doc_k[key] == row[u].doc);
           sc[n][e] = see ? x : -INFINITY;
           mx[u] = fmaxf(mx[u], sc[n][e]);
         }
@@ -343,12 +343,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0 && broken && a.status != nullptr) report_error(a.status, FVATTN_ERR_TIMEOUT, 500 + bars->abort);
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool DOCS>
 cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!make_map_keys(&mk, a.k, a.ks, a, kBlock) || !make_map_keys(&mv, a.v, a.vs, a, kBlock)) return cudaErrorInvalidValue;
   const size_t smem = FewLayout<D>::kBytes + 1024;
-  auto* kernel = dense_few_kernel<D, CAP, BIAS>;
+  auto* kernel = dense_few_kernel<D, CAP, BIAS, DOCS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr{};
@@ -366,11 +366,16 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, mk, mv, a);
 }
 
+template <int D, bool DOCS>
+cudaError_t launch_docs(const DenseArgs& a, cudaStream_t st) {
+  const bool cap = a.cap > 0.f, bias = a.mask.slopes != nullptr;
+  if (cap) return bias ? launch<D, true, true, DOCS>(a, st) : launch<D, true, false, DOCS>(a, st);
+  return bias ? launch<D, false, true, DOCS>(a, st) : launch<D, false, false, DOCS>(a, st);
+}
+
 template <int D>
 cudaError_t launch_d(const DenseArgs& a, cudaStream_t st) {
-  const bool cap = a.cap > 0.f, bias = a.mask.slopes != nullptr;
-  if (cap) return bias ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
-  return bias ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
+  return a.mask.doc_k != nullptr ? launch_docs<D, true>(a, st) : launch_docs<D, false>(a, st);
 }
 
 }  // namespace

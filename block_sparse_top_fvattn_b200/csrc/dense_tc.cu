@@ -66,7 +66,7 @@ struct FwdBars {
 
 static_assert(sizeof(FwdBars) <= 256, "the barriers fit their place");
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool DOCS>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     dense_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const DenseArgs a, const int qpt,
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (a.mask.doc_q != nullptr) {
+  if (DOCS) {
     for (int i = i0 + threadIdx.x; i < i1; i += kWarps * 32) {
       const int doc = a.mask.doc_q[(int64_t)b * a.Sq + i];
       if (doc >= 0) {
@@ -131,15 +131,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     __syncthreads();
   }
   const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
-  const int2* docs = a.doc_blocks_k != nullptr ? a.doc_blocks_k + (int64_t)b * ((a.Sk + kBlock - 1) / kBlock) : nullptr;
-  BlockWalk walk(docs, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
+  const int2* docs = DOCS ? a.doc_blocks_k + (int64_t)b * ((a.Sk + kBlock - 1) / kBlock) : nullptr;
+  BlockWalk<DOCS> walk(docs, key0 / kBlock, (key1 + kBlock - 1) / kBlock, bars->doc_lo, bars->doc_hi);
 
   if (warp == 0) {
     // ------------------------------------------------------------ loader
     // K_g as soon as the S that read its stage is done, then V_{g-1} once the P V that read its is.
     int k_par[NS] = {-1, -1};
     bool q_armed = false;
-    const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+    const int32_t* doc_k = DOCS ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
     auto load_k = [&](uint32_t g, int j) -> bool {
       const int st = g % NS;
       if (!warp_wait(&bars->s_full[st], ((g / NS) & 1) ^ 1, abort)) return false;
@@ -152,12 +152,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       k_par[1] = st == 1 ? (int)((g / NS) & 1) : k_par[1];
       return true;
     };
-    auto load_v = [&](uint32_t g, int j) -> bool {
+    auto load_v = [&](uint32_t g, int j, bool padded) -> bool {
       const int st = g % NS;
       unsigned char* dst = sV + st * L::kKBytes;
       if (!warp_wait(&bars->pv_done[st], ((g / NS) & 1) ^ 1, abort)) return false;
       // keys that do not exist although their memory does: zeros, whatever it holds (0 * NaN would reach O)
-      if ((seq.kv < a.Sk && (j + 1) * kBlock > seq.kv) || (docs != nullptr && docs[j].x < 0)) {
+      if ((seq.kv < a.Sk && (j + 1) * kBlock > seq.kv) || padded) {
         copy_keys<D>(dst, static_cast<const __nv_bfloat16*>(a.v) + (int64_t)b * a.vs.b + (int64_t)h * a.vs.h, a.vs.s,
                      j * kBlock, kBlock, seq.kv, doc_k, lane, 32);
         tc::fence_proxy_async_smem();
@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     };
     uint32_t g = 0;
     int before = -1;
+    bool padded = false;         // block `before` has padding keys
     bool ok = true;
     for (int j; ok && (j = walk.next(lane)) >= 0; ++g) {
       if (g == 0 && lane == 0) {
@@ -180,10 +181,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         q_armed = true;
         for (int c = 0; c < D / 64; ++c) tc::tma_load_5d(sQ + c * L::kQChunk, &tmQ, &bars->q_full, c * 64, 0, i0, h, b);
       }
-      ok = load_k(g, j) && (g == 0 || load_v(g - 1, before));
+      ok = load_k(g, j) && (g == 0 || load_v(g - 1, before, padded));
       before = j;
+      padded = DOCS && walk.doc().x < 0;
     }
-    if (!ok || (g > 0 && !load_v(g - 1, before))) fail(&bars->abort, 3);
+    if (!ok || (g > 0 && !load_v(g - 1, before, padded))) fail(&bars->abort, 3);
     // no copy may still be writing shared memory when the CTA leaves
     if (lane == 0) {
       if (q_armed) tc::mbar_wait_drain(&bars->q_full, 0, kWaitLimit);
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     DenseRow row{0, 0, 0, 0.f};
     if (valid) row = dense_row(a, seq, b, hq, i);
     const bool live_warp = __any_sync(0xffffffffu, valid);
-    const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
+    const int32_t* doc_k = DOCS ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
     const ScoreMap<CAP, BIAS> map(a, row);
     float mrow = -INFINITY;
     uint64_t lsum = f2(0.f, 0.f);
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         tc::tmem_ld_wait();
         map.apply(lo, row.pos - j * kBlock);
         map.apply(hi, row.pos - j * kBlock - 32);
-        const uint64_t see = visible64(row, doc_k, docs != nullptr ? docs[j] : make_int2(0, 0), j * kBlock, a.Sk, lane);
+        const uint64_t see = visible64<DOCS>(row, doc_k, walk.doc(), j * kBlock, a.Sk, lane);
         if (__any_sync(0xffffffffu, see != ~0ull)) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   }
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool DOCS>
 cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   const int qpt = kTileRows / a.G;
   CUtensorMap mq, mk, mv;
@@ -419,7 +421,7 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
       !make_map_keys(&mv, a.v, a.vs, a, kBlock))
     return cudaErrorInvalidValue;
   const size_t smem = FwdLayout<D>::kBytes + 1024;
-  auto* kernel = dense_tc_kernel<D, CAP, BIAS>;
+  auto* kernel = dense_tc_kernel<D, CAP, BIAS, DOCS>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const TileOrder order = tile_order(a, (a.Sq + qpt - 1) / qpt * a.splits, a.causal);
@@ -429,11 +431,16 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <int D, bool DOCS>
+cudaError_t launch_docs(const DenseArgs& a, cudaStream_t st) {
+  const bool cap = a.cap > 0.f, bias = a.mask.slopes != nullptr;
+  if (cap) return bias ? launch<D, true, true, DOCS>(a, st) : launch<D, true, false, DOCS>(a, st);
+  return bias ? launch<D, false, true, DOCS>(a, st) : launch<D, false, false, DOCS>(a, st);
+}
+
 template <int D>
 cudaError_t launch_d(const DenseArgs& a, cudaStream_t st) {
-  const bool cap = a.cap > 0.f, bias = a.mask.slopes != nullptr;
-  if (cap) return bias ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
-  return bias ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
+  return a.mask.doc_k != nullptr ? launch_docs<D, true>(a, st) : launch_docs<D, false>(a, st);
 }
 
 }  // namespace

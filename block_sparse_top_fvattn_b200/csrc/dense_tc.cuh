@@ -105,40 +105,50 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* out, __nv_bfloat16* r
 __device__ __forceinline__ int doc_low(int2 v) { return v.x & 0x7fffffff; }
 __device__ __forceinline__ bool doc_uniform(int2 v) { return v.x == v.y; }      // one document, no padding
 
-// Ascending walk over the blocks [j, end) of tokens whose documents meet the range [lo, hi] (every block
-// without documents). Used by whole warps: with documents a warp tests 32 blocks at a time.
+// Ascending walk over the blocks [j, end) of tokens; with documents, over those whose documents meet the
+// range [lo, hi]. Used by whole warps: a warp tests 32 blocks at a time.
+template <bool DOCS>
 struct BlockWalk {
-  const int2* docs;       // null without documents
+  int j, end;
+  __device__ __forceinline__ BlockWalk(const int2*, int begin, int stop, int, int) : j(begin), end(stop) {}
+  __device__ __forceinline__ int next(int) { return j < end ? j++ : -1; }
+  __device__ __forceinline__ int2 doc() const { return make_int2(0, 0); }
+  __device__ __forceinline__ int count(int) const { return max(0, end - j); }
+};
+template <>
+struct BlockWalk<true> {
+  const int2* docs;
   int j, end, lo, hi;
   uint32_t word;          // blocks of the current window that are left
   int base;               // its first block
+  int2 held;              // documents of block base + lane
+  int at;                 // the last block that next() gave, counted from base
 
   __device__ __forceinline__ BlockWalk(const int2* docs_, int begin, int stop, int lo_, int hi_)
-      : docs(docs_), j(begin), end(stop), lo(lo_), hi(hi_), word(0), base(begin) {}
-  __device__ __forceinline__ uint32_t window(int at, int lane) const {
-    bool see = false;
-    if (at + lane < end) {
-      const int2 v = docs[at + lane];
-      see = doc_low(v) <= hi && v.y >= lo;
-    }
-    return __ballot_sync(0xffffffffu, see);
+      : docs(docs_), j(begin), end(stop), lo(lo_), hi(hi_), word(0), base(begin), held(make_int2(0, 0)), at(0) {}
+  __device__ __forceinline__ uint32_t window(int first, int lane, int2& v) const {
+    v = first + lane < end ? docs[first + lane] : make_int2(0x7fffffff, -1);
+    return __ballot_sync(0xffffffffu, doc_low(v) <= hi && v.y >= lo);
   }
   __device__ __forceinline__ int next(int lane) {
-    if (docs == nullptr) return j < end ? j++ : -1;
     while (word == 0) {
       if (j >= end) return -1;
       base = j;
-      word = window(j, lane);
+      word = window(j, lane, held);
       j += 32;
     }
-    const int c = __ffs(word) - 1;
+    at = __ffs(word) - 1;
     word &= word - 1;
-    return base + c;
+    return base + at;
+  }
+  // The documents of the block that next() gave (they are in a lane's registers: no load).
+  __device__ __forceinline__ int2 doc() const {
+    return make_int2(__shfl_sync(0xffffffffu, held.x, at), __shfl_sync(0xffffffffu, held.y, at));
   }
   __device__ __forceinline__ int count(int lane) const {
-    if (docs == nullptr) return max(0, end - j);
     int n = 0;
-    for (int at = j; at < end; at += 32) n += __popc(window(at, lane));
+    int2 v;
+    for (int first = j; first < end; first += 32) n += __popc(window(first, lane, v));
     return n;
   }
 };
@@ -163,10 +173,11 @@ __device__ __forceinline__ uint64_t same_document(int d0, int d1, int mine) {
 
 // Bit c: key first + c is visible to this lane's row; v: the documents of the block it lies in. The
 // whole warp takes part.
+template <bool DOCS>
 __device__ __forceinline__ uint64_t visible64(const DenseRow& row, const int32_t* doc_k, int2 v, int first, int Sk,
                                               int lane) {
   uint64_t see = low64(row.limit - first);
-  if (doc_k != nullptr) {
+  if (DOCS) {
     if (doc_uniform(v)) {
       if (v.y != row.doc) see = 0ull;
     } else {

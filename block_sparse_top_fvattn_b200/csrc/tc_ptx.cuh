@@ -165,6 +165,16 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_
       : "memory");
 }
 
+// Registers per thread of the four warps of a warpgroup, all of which come here.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // True in one lane of a converged warp, always the same one. A block under it keeps its operands in
 // uniform registers: an MMA then costs about 40 cycles of issue, under `lane == 0` about 60 (measured
 // alone; over 100 beside sixteen busy warps).
