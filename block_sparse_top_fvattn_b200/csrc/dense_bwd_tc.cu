@@ -23,6 +23,7 @@
 //
 // Every wait is bounded; one that runs out stops every role without leaving a copy or product in
 // flight, is reported in the status word, and makes the CTA's results NaN.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -32,6 +33,8 @@
 #include "dense_tc.cuh"
 #include "tc_ptx.cuh"
 #include "tmap.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace fv {
 
@@ -116,6 +119,10 @@ struct DkvLayout {
   static constexpr int kOffStats = kOffG + kStagesG * kRowTile;
   static constexpr int kOffBar = kOffStats + 4 * (int)sizeof(RowStats);
   static constexpr int kBytes = kOffBar + 512;
+  // at the end, where a cluster joins its CTAs' results: [dV, dK][key][dim] fp32 over the tiles, rows four
+  // floats longer than D (lanes write rows: no two in one bank)
+  static constexpr int kLdOut = D + 4;
+  static_assert(2 * kT * kLdOut * 4 <= kOffStats, "the results fit the tiles");
   // TMEM: scores of even and odd steps, dP of even and odd steps, the results
   static constexpr uint32_t kColS = 0, kColDp = 128, kColV = 256, kColK = 384;
 };
@@ -133,6 +140,21 @@ struct DkvBars {
 
 static_assert(sizeof(DkvBars) <= 512, "the barriers fit their place");
 
+// One CTA's share of a walk: of its steps every a.cluster-th, from the CTA's rank in the cluster on.
+template <bool DOCS>
+struct SharedWalk : BlockWalk<DOCS> {
+  int skip;      // steps of the others before the next of its own
+  __device__ __forceinline__ SharedWalk(const BlockWalk<DOCS>& w, int rank) : BlockWalk<DOCS>(w), skip(rank) {}
+  __device__ __forceinline__ int next(int lane, int of) {
+    for (; skip > 0; --skip) BlockWalk<DOCS>::next(lane);
+    skip = of - 1;
+    return BlockWalk<DOCS>::next(lane);
+  }
+  __device__ __forceinline__ int count(int lane, int of) const {
+    return max(0, BlockWalk<DOCS>::count(lane) - skip + of - 1) / of;
+  }
+};
+
 template <int D, bool CAP, bool BIAS, bool DOCS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
@@ -146,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
   int x, bh;
-  tile_of(order, blockIdx.x, x, bh);        // the first keys are seen by the most rows under an order
+  tile_of(order, blockIdx.x / a.cluster, x, bh);      // the first keys are seen by the most rows under an order
   const int b = bh / a.Hkv, h = bh - b * a.Hkv, j0 = x * kT;
   const DenseSeq seq = dense_seq(a, b);
   const int32_t* doc_q = DOCS ? a.mask.doc_q + (int64_t)b * a.Sq : nullptr;
@@ -212,8 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     first = max(0, min(j0 - seq.q0, a.Sq)) / qpt;      // query i sees key j0 when q0 + i >= j0
   }
   const int2* tile_docs = DOCS ? a.doc_blocks_q + (int64_t)b * tiles : nullptr;
-  BlockWalk<DOCS> walk(tile_docs, first, tiles, bars->doc_lo, bars->doc_hi);
-  const uint32_t n = (uint32_t)walk.count(lane);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int share = a.cluster;
+  SharedWalk<DOCS> walk(BlockWalk<DOCS>(tile_docs, first, tiles, bars->doc_lo, bars->doc_hi), (int)cluster.block_rank());
+  const uint32_t n = (uint32_t)walk.count(lane, share);
 
   if (warp >= kWork) {
     tc::regs_down<kRegsOther>();
@@ -247,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = true;
-      for (int t; ok && (t = walk.next(lane)) >= 0; ++g) {
+      for (int t; ok && (t = walk.next(lane, share)) >= 0; ++g) {
         const uint32_t sq = g % kStagesQ, sg = g % kStagesG;
         const bool pad = DOCS && walk.doc().x < 0;
         ok = load(tmQ, a.q, a.qs, &bars->q_full[sq], &bars->q_empty[sq], ((g / kStagesQ) & 1) ^ 1,
@@ -465,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int jend = min(kT, seq.kv - j0);
     const bool one_doc = bars->doc_lo == bars->doc_hi && !bars->doc_pad;
     bool ok = true;
-    int t = walk.next(lane);
-    if (group == 1) t = walk.next(lane);
+    int t = walk.next(lane, share);
+    if (group == 1) t = walk.next(lane, share);
     int2 docs = t >= 0 ? walk.doc() : make_int2(0, 0);       // of step t
     if (t >= 0) fetch(t);
     for (uint32_t turn = 0; t >= 0; ++turn) {
@@ -474,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i0 = t * qpt;
       put(st);
       named_sync(1 + group, kWork / 2 * 32);      // after an abort too: every warp takes all its turns
-      walk.next(lane);                            // the other group's
-      const int next = walk.next(lane);
+      walk.next(lane, share);                            // the other group's
+      const int next = walk.next(lane, share);
       const int2 next_docs = next >= 0 ? walk.doc() : make_int2(0, 0);
       if (next >= 0) fetch(next);
       see = (uint32_t)(low64(min(qpt, a.Sq - i0) * a.G - col0) & 0xffffffffull);
@@ -534,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const fvattn_strides& ss = group == 0 ? a.dvs : a.dks;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(group == 0 ? a.dv : a.dk) + (int64_t)b * ss.b + (int64_t)h * ss.h +
                          (int64_t)j * ss.s;
+    float* shared_row = reinterpret_cast<float*>(smem) + (group * kT + r) * L::kLdOut;
 #pragma unroll 1
     for (int cc = part_d * (D / 64); cc < (part_d + 1) * (D / 64); ++cc) {
       uint32_t o[32];
@@ -547,8 +572,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
-      if (j < a.Sk) store32(dst + cc * 32, o, by);
+      if (share == 1) {
+        if (j < a.Sk) store32(dst + cc * 32, o, by);
+      } else {
+        // over the tiles: every product of the CTA is done
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(shared_row + cc * 32 + e) =
+              make_float4(__uint_as_float(o[e]) * by, __uint_as_float(o[e + 1]) * by, __uint_as_float(o[e + 2]) * by,
+                          __uint_as_float(o[e + 3]) * by);
+      }
     }
+  }
+  if (share > 1) {
+    // the cluster's sums, in the order of the ranks; each CTA writes its part of the keys
+    cluster.sync();
+    const int rows = kT / share, row0 = (int)cluster.block_rank() * rows;
+    for (int i = threadIdx.x; i < 2 * rows * (D / 8); i += kThreads) {
+      const int which = i / (rows * (D / 8)), k = i % (rows * (D / 8)), row = row0 + k / (D / 8), d = k % (D / 8) * 8;
+      float acc[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      for (int rank = 0; rank < share; ++rank) {
+        const float* p = cluster.map_shared_rank(reinterpret_cast<float*>(smem), rank) + (which * kT + row) * L::kLdOut + d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += p[e];
+      }
+      if (j0 + row < a.Sk) {
+        const fvattn_strides& ss = which == 0 ? a.dvs : a.dks;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which == 0 ? a.dv : a.dk) + (int64_t)b * ss.b +
+                             (int64_t)h * ss.h + (int64_t)(j0 + row) * ss.s + d;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
+                                                    pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
+      }
+    }
+    cluster.sync();                      // a CTA's shared memory is read until here
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -907,9 +965,24 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const TileOrder order = tile_order(a, (a.Sk + kT - 1) / kT, a.causal);
-    if ((int64_t)order.tiles * order.heads > 0x7fffffff) return cudaErrorInvalidValue;
-    kernel<<<order.tiles * order.heads, kThreads, smem, st>>>(mqr, mgr, mk, mv, a, qpr, order);
-    e = cudaGetLastError();
+    // Where the key tiles leave half of the 148 SMs idle, a cluster shares a tile's steps, four each at least.
+    const int64_t grid = (int64_t)order.tiles * order.heads, steps = (a.Sq + qpr - 1) / qpr;
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    DenseArgs c = a;
+    c.cluster = 1;
+    while (c.cluster < 8 && grid * c.cluster * 2 <= 148 && steps >= c.cluster * 8) c.cluster *= 2;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)c.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(grid * c.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, mqr, mgr, mk, mv, c, qpr, order);
     if (e != cudaSuccess) return e;
   }
   auto* kernel = dense_dq_tc_kernel<D, CAP, BIAS, DOCS>;
