@@ -300,7 +300,8 @@ int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_
   cudaError_t e = cudaSuccess;
   if (shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
     a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
-    e = launch_dense_docs(a.mask.doc_k, a.doc_blocks_k, a.B, a.Sk, kBlock, s);
+    a.doc_size_k = kBlock;
+    e = launch_dense_prepare(a, shape->dtype, s);
   }
   if (e == cudaSuccess)
     e = shape->dtype == FVATTN_F32 ? launch_dense_f32(a, s)
@@ -344,13 +345,13 @@ int fvattn_dense_attn_bwd(const void* dout, const void* q, const void* k, const 
   a.delta = reinterpret_cast<float*>(ws + w.delta);
   a.status = status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_dense_delta(a, shape->dtype, s);
-  if (e == cudaSuccess && shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
+  if (shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
     a.doc_blocks_q = reinterpret_cast<int2*>(ws + w.docs_q);
     a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
-    e = launch_dense_docs(a.mask.doc_q, a.doc_blocks_q, a.B, a.Sq, kBwdRows / a.G, s);
-    if (e == cudaSuccess) e = launch_dense_docs(a.mask.doc_k, a.doc_blocks_k, a.B, a.Sk, kBwdKeys, s);
+    a.doc_size_q = kBwdRows / a.G;
+    a.doc_size_k = kBwdKeys;
   }
+  cudaError_t e = launch_dense_prepare(a, shape->dtype, s);
   if (e == cudaSuccess) e = shape->dtype == FVATTN_BF16 ? launch_dense_bwd_tc(a, s) : launch_dense_f32_bwd(a, s);
   return cuda_status(e);
 }

@@ -70,25 +70,37 @@ __device__ inline int debug_row_check(const int32_t* row_ptr, const int32_t* col
 }
 #endif
 
-// A kernel launched by launch_after_previous may start while the one before it on its stream still
-// runs; it waits here until that has ended and its writes are visible, before it touches anything that
-// the other may write or read. allow_next_grid, in the one before, lets it start early.
+// A kernel launched early (launch_with) may start while the one before it on its stream still runs; it
+// waits here until that has ended and its writes are visible, before it touches anything that the other
+// may write or read and before it takes tensor memory that the other may still ask for. Every kernel so
+// launched waits: the one after it counts on that. allow_next_grid, in the one before, lets it start.
 __device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A launch in clusters of `cluster` CTAs along x; `early`: one that begins with wait_for_previous_grid.
 template <typename... P, typename... A>
-cudaError_t launch_after_previous(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
-                                  A... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_with(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, int cluster,
+                        bool early, A... args) {
+  cudaLaunchAttribute attr[2] = {};
+  int n = 0;
+  if (cluster > 0) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (early) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 

@@ -30,9 +30,10 @@ struct DenseArgs {
   int cluster, parts;             // ranges joined within a cluster; what is left to join through memory
   float *part_o, *part_lse;       // parts > 1: [parts][B][Hq][Sq][d] and [parts][B][Hq][Sq]
   float* delta;                   // backward: [B][Hq][Sq], sum_d out * dout
-  // Documents of blocks of tokens (dense_doc_kernel), null without documents: of the keys in blocks of
+  // Documents of blocks of tokens (dense_prepare_kernel), null without documents: of the keys in blocks of
   // 64 (forward) or 128 (backward), of the queries in steps of dK and dV (backward).
   int2 *doc_blocks_q, *doc_blocks_k;
+  int doc_size_q, doc_size_k;
   int32_t* status;
 };
 
@@ -80,14 +81,14 @@ __device__ __forceinline__ DenseRow dense_row(const DenseArgs& a, const DenseSeq
 }
 
 // Launchers. Each returns the launch's error.
-cudaError_t launch_dense_docs(const int32_t* doc, int2* blocks, int B, int S, int block, cudaStream_t st);
 cudaError_t launch_dense_bwd_tc(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_tc(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_few(const DenseArgs& a, cudaStream_t st);
 constexpr int kFewRows = 16;      // the most rows of a key head that launch_dense_few takes
 cudaError_t launch_dense_f32(const DenseArgs& a, cudaStream_t st);
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st);
-cudaError_t launch_dense_delta(const DenseArgs& a, int dtype, cudaStream_t st);
+// delta where a.delta is set, the documents of blocks where a.doc_blocks_q and a.doc_blocks_k are.
+cudaError_t launch_dense_prepare(const DenseArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_dense_f32_bwd(const DenseArgs& a, cudaStream_t st);
 
 }  // namespace fv

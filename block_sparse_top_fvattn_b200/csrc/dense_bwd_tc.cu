@@ -167,6 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   DkvBars* bars = reinterpret_cast<DkvBars*>(smem + L::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
+  wait_for_previous_grid();
+  allow_next_grid();
   int x, bh;
   tile_of(order, blockIdx.x / a.cluster, x, bh);      // the first keys are seen by the most rows under an order
   const int b = bh / a.Hkv, h = bh - b * a.Hkv, j0 = x * kT;
@@ -654,6 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   DqBars* bars = reinterpret_cast<DqBars*>(smem + L::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
+  wait_for_previous_grid();
+  allow_next_grid();
   int x, bh;
   tile_of(order, blockIdx.x, x, bh);
   const int t = order.tiles - 1 - x, b = bh / a.Hkv, h = bh - b * a.Hkv;      // the longest tiles first
@@ -971,18 +975,8 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
     DenseArgs c = a;
     c.cluster = 1;
     while (c.cluster < 8 && grid * c.cluster * 2 <= 148 && steps >= c.cluster * 8) c.cluster *= 2;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)c.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(grid * c.cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, mqr, mgr, mk, mv, c, qpr, order);
+    e = launch_with(kernel, dim3((unsigned)(grid * c.cluster)), kThreads, smem, st, c.cluster, true, mqr, mgr, mk, mv, c, qpr,
+                    order);
     if (e != cudaSuccess) return e;
   }
   auto* kernel = dense_dq_tc_kernel<D, CAP, BIAS, DOCS>;
@@ -991,8 +985,8 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const TileOrder order = tile_order(a, (a.Sq + qpt - 1) / qpt, a.causal);
   if ((int64_t)order.tiles * order.heads > 0x7fffffff) return cudaErrorInvalidValue;
-  kernel<<<order.tiles * order.heads, kThreads, smem, st>>>(mq, mg, mk, mv, a, qpt, order);
-  return cudaGetLastError();
+  return launch_with(kernel, dim3((unsigned)(order.tiles * order.heads)), kThreads, smem, st, 0, true, mq, mg, mk, mv, a, qpt,
+                     order);
 }
 
 template <int D, bool DOCS>

@@ -1,5 +1,6 @@
 // Attention over all keys in fp32 on the CUDA cores, forward and backward, and the two small
-// kernels that the bf16 path shares: the join of split keys and the row sums of out * dout.
+// kernels that the bf16 path shares: the join of split keys, and what the other kernels need first (the row sums
+// of out * dout, the documents of blocks of tokens).
 //
 //   s_ij = cap tanh(scale q_i.k_j / cap) - slope |p_i - j|,  P = softmax over the visible j,
 //   out = P V,  lse_i = log sum_j exp(s_ij)
@@ -294,10 +295,10 @@ __global__ void __launch_bounds__(kThreads) dense_combine_kernel(const DenseArgs
 // delta = sum_d (out + rest) dout; eight elements per lane, d / 8 lanes per row. Padding queries get 0,
 // whatever they hold.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) dense_delta_kernel(const DenseArgs a) {
+__device__ __forceinline__ void row_delta(const DenseArgs& a, int64_t block) {
   constexpr int LPR = D / 8;
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
-  const int64_t flat = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+  const int64_t flat = block * (kThreads / LPR) + threadIdx.x / LPR;
   const int l = threadIdx.x % LPR;
   float acc = 0.f;
   if (flat < rows) {
@@ -321,18 +322,18 @@ __global__ void __launch_bounds__(kThreads) dense_delta_kernel(const DenseArgs a
   if (l == 0 && flat < rows) a.delta[flat] = acc;
 }
 
-// The documents of each block of `block` tokens of doc [B][S], one warp per block: x = the lowest
+// The documents of each block of `size` tokens of doc [B][S], one warp per block: x = the lowest
 // number, with the sign bit set when the block has padding tokens (0x7fffffff without any document),
 // y = the highest (-1 without any).
-__global__ void __launch_bounds__(kThreads) dense_doc_kernel(const int32_t* doc, int2* blocks, int B, int S, int block) {
-  const int nb = (S + block - 1) / block, lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+__device__ __forceinline__ void block_docs(const int32_t* doc, int2* blocks, int B, int S, int size, int64_t block) {
+  const int nb = (S + size - 1) / size, lane = threadIdx.x & 31;
+  const int64_t w = block * (kThreads / 32) + (threadIdx.x >> 5);
   if (w >= (int64_t)B * nb) return;
   const int64_t b = w / nb, j = w - b * nb;
   int lo = 0x7fffffff, hi = -1;
   bool pad = false;
-  for (int u = lane; u < block; u += 32) {
-    const int64_t t = j * block + u;
+  for (int u = lane; u < size; u += 32) {
+    const int64_t t = j * size + u;
     if (t >= S) break;
     const int v = doc[b * S + t];
     if (v < 0) {
@@ -346,6 +347,20 @@ __global__ void __launch_bounds__(kThreads) dense_doc_kernel(const int32_t* doc,
   hi = __reduce_max_sync(0xffffffffu, hi);
   pad = __any_sync(0xffffffffu, pad);
   if (lane == 0) blocks[w] = make_int2(pad ? (int)((uint32_t)lo | 0x80000000u) : lo, hi);
+}
+
+// What the other kernels of a call need first, in one launch: CTAs [0, q0) the rows' delta, [q0, k0) the
+// documents of the queries' blocks, the rest those of the keys'.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dense_prepare_kernel(const DenseArgs a, int64_t q0, int64_t k0) {
+  allow_next_grid();
+  const int64_t x = blockIdx.x;
+  if (x < q0)
+    row_delta<T, D>(a, x);
+  else if (x < k0)
+    block_docs(a.mask.doc_q, a.doc_blocks_q, a.B, a.Sq, a.doc_size_q, x - q0);
+  else
+    block_docs(a.mask.doc_k, a.doc_blocks_k, a.B, a.Sk, a.doc_size_k, x - k0);
 }
 
 // Probability and score gradient of one pair: p = exp(s - lse), ds = p (dp - delta) cap' scale.
@@ -524,10 +539,6 @@ cudaError_t bwd_d(const DenseArgs& a, cudaStream_t st) {
   return run(dense_dkv_kernel<T, D>, dim3((unsigned)((a.Sk + kT - 1) / kT), a.Hkv, a.B), smem, a, st);
 }
 
-unsigned delta_blocks(const DenseArgs& a) {
-  const int64_t per = kThreads / (a.d / 8);
-  return (unsigned)(((int64_t)a.B * a.Hq * a.Sq + per - 1) / per);
-}
 unsigned warp_rows(const DenseArgs& a) {
   return (unsigned)(((int64_t)a.B * a.Hq * a.Sq + kThreads / 32 - 1) / (kThreads / 32));
 }
@@ -540,28 +551,27 @@ cudaError_t launch_dense_f32(const DenseArgs& a, cudaStream_t st) {
 cudaError_t launch_dense_f32_bwd(const DenseArgs& a, cudaStream_t st) {
   return a.d == 128 ? bwd_d<float, 128>(a, st) : bwd_d<float, 64>(a, st);
 }
-cudaError_t launch_dense_docs(const int32_t* doc, int2* blocks, int B, int S, int block, cudaStream_t st) {
-  const int64_t warps = (int64_t)B * ((S + block - 1) / block);
-  dense_doc_kernel<<<(unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(doc, blocks, B, S,
-                                                                                                 block);
-  return cudaGetLastError();
+cudaError_t launch_dense_prepare(const DenseArgs& a, int dtype, cudaStream_t st) {
+  auto warps = [](int64_t B, int64_t S, int64_t size) {
+    return (B * ((S + size - 1) / size) + kThreads / 32 - 1) / (kThreads / 32);
+  };
+  const int64_t per = kThreads / (a.d / 8);
+  const int64_t q0 = a.delta != nullptr ? ((int64_t)a.B * a.Hq * a.Sq + per - 1) / per : 0;
+  const int64_t k0 = q0 + (a.doc_blocks_q != nullptr ? warps(a.B, a.Sq, a.doc_size_q) : 0);
+  const int64_t end = k0 + (a.doc_blocks_k != nullptr ? warps(a.B, a.Sk, a.doc_size_k) : 0);
+  if (end > 0x7fffffff) return cudaErrorInvalidValue;
+  auto go = [&](auto kernel) {
+    kernel<<<(unsigned)end, kThreads, 0, st>>>(a, q0, k0);
+    return cudaGetLastError();
+  };
+  if (dtype == FVATTN_F32) return a.d == 128 ? go(dense_prepare_kernel<float, 128>) : go(dense_prepare_kernel<float, 64>);
+  return a.d == 128 ? go(dense_prepare_kernel<__nv_bfloat16, 128>) : go(dense_prepare_kernel<__nv_bfloat16, 64>);
 }
 
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, cudaStream_t st) {
-  auto go = [&](auto kernel) { return launch_after_previous(kernel, dim3(warp_rows(a)), kThreads, 0, st, a); };
+  auto go = [&](auto kernel) { return launch_with(kernel, dim3(warp_rows(a)), kThreads, 0, st, 0, true, a); };
   if (dtype == FVATTN_F32) return a.d == 128 ? go(dense_combine_kernel<float, 128>) : go(dense_combine_kernel<float, 64>);
   return a.d == 128 ? go(dense_combine_kernel<__nv_bfloat16, 128>) : go(dense_combine_kernel<__nv_bfloat16, 64>);
-}
-
-cudaError_t launch_dense_delta(const DenseArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == FVATTN_F32) {
-    if (a.d == 128) dense_delta_kernel<float, 128><<<delta_blocks(a), kThreads, 0, st>>>(a);
-    else dense_delta_kernel<float, 64><<<delta_blocks(a), kThreads, 0, st>>>(a);
-  } else {
-    if (a.d == 128) dense_delta_kernel<__nv_bfloat16, 128><<<delta_blocks(a), kThreads, 0, st>>>(a);
-    else dense_delta_kernel<__nv_bfloat16, 64><<<delta_blocks(a), kThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
 }
 
 }  // namespace fv

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   FewBars* bars = reinterpret_cast<FewBars*>(smem + L::kOffBar);
   __shared__ FewStats cta;
+  if (DOCS) wait_for_previous_grid();              // the documents of the blocks
   allow_next_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
@@ -351,19 +352,8 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   auto* kernel = dense_few_kernel<D, CAP, BIAS, DOCS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)a.cluster;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.splits, (unsigned)(a.B * a.Hkv));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mk, mv, a);
+  return launch_with(kernel, dim3((unsigned)a.splits, (unsigned)(a.B * a.Hkv)), kThreads, smem, st, a.cluster, DOCS, mk, mv,
+                     a);
 }
 
 template <int D, bool DOCS>

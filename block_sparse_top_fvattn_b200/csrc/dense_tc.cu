@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   unsigned char* sV = smem + L::kOffV;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
+  if (DOCS) wait_for_previous_grid();      // the documents of the blocks
   allow_next_grid();
 
   int x, bh;
@@ -427,8 +428,7 @@ cudaError_t launch(const DenseArgs& a, cudaStream_t st) {
   const TileOrder order = tile_order(a, (a.Sq + qpt - 1) / qpt * a.splits, a.causal);
   const int64_t grid = (int64_t)order.tiles * order.heads;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  kernel<<<(unsigned)grid, kWarps * 32, smem, st>>>(mq, mk, mv, a, qpt, order);
-  return cudaGetLastError();
+  return launch_with(kernel, dim3((unsigned)grid), kWarps * 32, smem, st, 0, DOCS, mq, mk, mv, a, qpt, order);
 }
 
 template <int D, bool DOCS>

@@ -99,7 +99,7 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* out, __nv_bfloat16* r
   }
 }
 
-// The documents of a sequence's blocks of tokens (dense_doc_kernel): x = the lowest number, with the
+// The documents of a sequence's blocks of tokens (dense_prepare_kernel): x = the lowest number, with the
 // sign bit set when the block has padding tokens too (0x7fffffff without any document); y = the
 // highest (-1 without any).
 __device__ __forceinline__ int doc_low(int2 v) { return v.x & 0x7fffffff; }

@@ -383,7 +383,7 @@ cudaError_t bwd_d(const QkNormArgs& a, const fvattn_qk_shape& s, cudaStream_t st
     qk_norm_bwd_kernel<T, D, false><<<grid, kThreads, 0, st>>>(a, s, p.per, p.walk);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (a.dwq == nullptr && a.dwk == nullptr)) return e;
-  return launch_after_previous(qk_norm_sum_kernel, dim3(D / 8, 2), kSumThreads, 0, st, a, D, p.parts_q, p.parts_k);
+  return launch_with(qk_norm_sum_kernel, dim3(D / 8, 2), kSumThreads, 0, st, 0, true, a, D, p.parts_q, p.parts_k);
 }
 
 }  // namespace
