@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         l[0] *= alpha[0];
         l[1] *= alpha[1];
       }
-      uint32_t pf[4];
+      uint32_t pf[4], left[4];                      // P, and with rest what its rounding left
       const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -254,7 +254,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int u = 0; u < 2; ++u) {
           const float p0 = ex2(sc[n][2 * u] - base[u]), p1 = ex2(sc[n][2 * u + 1] - base[u]);
           l[u] += p0 + p1;
-          pf[n * 2 + u] = pack_bf16(p0, p1);
+          const uint32_t pk = pack_bf16(p0, p1);
+          pf[n * 2 + u] = pk;
+          left[n * 2 + u] = pack_bf16(p0 - __uint_as_float(pk << 16), p1 - __uint_as_float(pk & 0xffff0000u));
         }
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) {
@@ -262,6 +264,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         ldmatrix4_trans(va + tile_at(warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), n * 2 + (lane >> 4)), f);
         mma16816(o[2 * n], pf, f[0], f[1]);
         mma16816(o[2 * n + 1], pf, f[2], f[3]);
+        if (a.rest != nullptr) {
+          mma16816(o[2 * n], left, f[0], f[1]);
+          mma16816(o[2 * n + 1], left, f[2], f[3]);
+        }
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->empty[s]);

@@ -16,11 +16,15 @@
 // keys are split over CTAs, and the partial results are joined by a second kernel.
 //
 // Rounding P to bf16 is what the second product's operands need; the row sums are of the unrounded P.
+// With rest (the output to 16 bits, for the gradients) P goes in as two bf16 terms, the second of them
+// what the rounding of the first left, behind it in the S buffer, and the second product is made twice.
 //
 // Every wait is bounded; one that runs out stops every role without leaving a copy or product in
 // flight, is reported in the status word, and makes the tile's rows NaN.
 #include <cuda.h>
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "dense.cuh"
 #include "dense_tc.cuh"
@@ -221,6 +225,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           for (int kk = 0; kk < kBlock / 16; ++kk)
             tc::mma_f16_tmem_a(tbase + L::kColO, tbase + pb * kBlock + kk * 8, bd + ((kk * 16 * 128) >> 4), idO,
                                kk > 0 ? 1u : (uint32_t)(g > 0));
+          if (a.rest != nullptr) {
+#pragma unroll
+            for (int kk = 0; kk < kBlock / 16; ++kk)
+              tc::mma_f16_tmem_a(tbase + L::kColO, tbase + pb * kBlock + 32 + kk * 8, bd + ((kk * 16 * 128) >> 4), idO, 1u);
+          }
           tc::mma_commit(&bars->pv_done[pb]);
         }
         __syncwarp();
@@ -320,8 +329,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         const float nm = mrow == -INFINITY ? 0.f : -mrow;
         const uint64_t negm = f2(nm, nm), after2 = f2(map.after, map.after);
         uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-        uint32_t packed[32];
-        auto weights = [&](const uint32_t (&x)[32], int at) {
+        // P of 32 keys over the S buffer, which is in registers; `two`: and what its rounding left behind it
+        auto weights = [&](const uint32_t (&x)[32], int at, auto two) {
+          uint32_t packed[16], left[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const uint64_t x2 = ffma2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), after2, negm);
@@ -329,13 +339,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             f2_split(x2, x0, x1);
             const float p0 = ex2(x0), p1 = ex2(x1);
             acc[c & 3] = fadd2(acc[c & 3], f2(p0, p1));
-            packed[at + c] = pack_bf16(p0, p1);
+            packed[c] = pack_bf16(p0, p1);
+            if (decltype(two)::value)
+              left[c] = pack_bf16(p0 - __uint_as_float(packed[c] << 16), p1 - __uint_as_float(packed[c] & 0xffff0000u));
           }
+          tc::tmem_st16(sp + at, packed);
+          if (decltype(two)::value) tc::tmem_st16(sp + 32 + at, left);
         };
-        weights(lo, 0);
-        weights(hi, 16);
+        if (a.rest != nullptr) {
+          weights(lo, 0, std::true_type{});
+          weights(hi, 16, std::true_type{});
+        } else {
+          weights(lo, 0, std::false_type{});
+          weights(hi, 16, std::false_type{});
+        }
         lsum = fadd2(lsum, fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])));
-        tc::tmem_st32(sp, packed);           // S_g is in registers
         tc::tmem_st_wait();
         tc::fence_before_sync();
       }

@@ -463,8 +463,8 @@ typedef struct {
  *   s_ij = cap(Q[i].K[j] * scale) - slope |p_i - j|.
  * A row that sees no key is written as zeros, with lse = -inf. lse: float [B, Hq, Sq] (dense), the
  * natural-log normaliser of each row, or NULL. rest: NULL, or a bf16 tensor like out (bf16 only)
- * that receives what out's rounding left over: out + rest is the result to 16 bits, which the
- * gradients of short or sharply peaked rows need. Few queries over many keys (single tokens over
+ * that receives what out's rounding left over: out + rest is the result to 16 bits (the weights
+ * then enter as two bf16 terms), which the gradients of short or sharply peaked rows need. Few queries over many keys (single tokens over
  * a cache) are split over the keys and joined. mask: NULL for none. workspace: 256-byte aligned,
  * fvattn_dense_attn_workspace_bytes(shape, mask) bytes (may be 0; (size_t)-1 on invalid
  * arguments; host only).
