@@ -376,11 +376,18 @@ class LazyRouter:
         layer = LazyRouter(RouteConfig(p=0.9), refresh_every=4)
         for step in range(n_steps):
             o = layer(q, k, v, step)
+
+    With dense_steps > 0 the first steps, which lay out the picture, attend to all keys (dense_attn)
+    and routing starts after them. from_projections takes the projections' [B, S, H, d] outputs and
+    norms and rotates queries and keys first (qk_norm_rope).
     """
 
-    def __init__(self, cfg: Optional[RouteConfig] = None, refresh_every: int = 4):
+    def __init__(self, cfg: Optional[RouteConfig] = None, refresh_every: int = 4, dense_steps: int = 0):
         if refresh_every < 1:
             raise ValueError("refresh_every must be >= 1")
+        if dense_steps < 0:
+            raise ValueError("dense_steps must be >= 0")
+        self.dense_steps = int(dense_steps)
         self.cfg = cfg or RouteConfig()
         self.refresh_every = int(refresh_every)
         self.csr: Optional[CsrBuffers] = None
@@ -397,6 +404,8 @@ class LazyRouter:
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, step: int, *,
                  out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        if step < self.dense_steps:
+            return dense_attn(q, k, v, out=out, stream=stream)
         if self.should_refresh(step, q.shape):
             B, H, S, _ = q.shape
             if self.csr is None or (self.csr.B, self.csr.H, self.csr.S) != (B, H, S):
@@ -407,3 +416,15 @@ class LazyRouter:
             self.last_refresh = step
             self.routed += 1
         return sparse_attn(q, k, v, self.csr, out=out, stream=stream)
+
+    def from_projections(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, step: int,
+                         q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                         cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, *,
+                         positions: Optional[torch.Tensor] = None, interleaved: bool = True, eps: float = 1e-6,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The layer on the projections q, k, v [B, S, H, d] (any strides with a contiguous last
+        dimension): norm and rotation of q and k (qk_norm_rope's arguments), then this step's attention.
+        Returns [B, H, S, d]."""
+        q, k = qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=positions, interleaved=interleaved, eps=eps)
+        v = v.transpose(1, 2)
+        return self(q, k, v if step < self.dense_steps else v.contiguous(), step, out=out)

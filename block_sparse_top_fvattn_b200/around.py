@@ -287,8 +287,8 @@ class AttnConfig:
     def check(self, q: torch.Tensor, Sk: int) -> None:
         """Raises ValueError unless the configuration fits queries q and Sk keys."""
         B, Hq, Sq, _ = q.shape
-        if not 0 <= self.softcap < float("inf"):
-            raise ValueError("softcap must be finite and >= 0")
+        if self.softcap != 0 and not 1e-20 <= self.softcap <= 1e20:
+            raise ValueError("softcap must be 0 or between 1e-20 and 1e20")
         if self.prefix_len is not None and not self.causal:
             raise ValueError("prefix_len needs causal=True")
         if (self.doc_q is None) != (self.doc_k is None):

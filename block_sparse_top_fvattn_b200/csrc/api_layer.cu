@@ -66,12 +66,13 @@ int validate_dense(const fvattn_dense_shape* s, const fvattn_dense_mask* m, bool
   if (s->B < 1 || s->Hq < 1 || s->Hkv < 1 || s->Sq < 1 || s->Sk < 1 || s->d < 1) return FVATTN_ERR_INVALID;
   if (s->dtype != FVATTN_BF16 && s->dtype != FVATTN_F32) return FVATTN_ERR_INVALID;
   if (isnan(s->scale) || isinf(s->scale)) return FVATTN_ERR_INVALID;
-  if (!(s->softcap >= 0.f) || isinf(s->softcap)) return FVATTN_ERR_INVALID;
+  // a cap's reciprocal and its base-2 exponents have to be numbers
+  if (s->softcap != 0.f && !(s->softcap >= 1e-20f && s->softcap <= 1e20f)) return FVATTN_ERR_INVALID;
   if (s->causal != 0 && s->causal != 1) return FVATTN_ERR_INVALID;
   if (s->Hq % s->Hkv != 0) return FVATTN_ERR_INVALID;
   if (s->d != 64 && s->d != 128) return FVATTN_ERR_UNSUPPORTED;
-  if (s->Hq / s->Hkv > 64 || s->B > 65535 || s->Hkv > 65535) return FVATTN_ERR_UNSUPPORTED;
-  if (s->Sq > kPosMax || s->Sk > kPosMax || s->Sq * (s->Hq / s->Hkv) > (int64_t)1 << 34) return FVATTN_ERR_UNSUPPORTED;
+  if (s->Hq / s->Hkv > 64 || s->B > 65535 || s->Hkv > 65535 || s->B * s->Hkv > 65535) return FVATTN_ERR_UNSUPPORTED;
+  if (s->Sq > kPosMax || s->Sk > kPosMax || s->Sq * (s->Hq / s->Hkv) > kPosMax) return FVATTN_ERR_UNSUPPORTED;
   if (!valid_strides(s->q, s->B, s->Hq, s->Sq, s->dtype) || !valid_strides(s->k, s->B, s->Hkv, s->Sk, s->dtype) ||
       !valid_strides(s->v, s->B, s->Hkv, s->Sk, s->dtype) || !valid_strides(s->o, s->B, s->Hq, s->Sq, s->dtype))
     return FVATTN_ERR_INVALID;
@@ -102,6 +103,7 @@ DenseArgs dense_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
   a.causal = s->causal;
   a.scale = s->scale > 0.f ? s->scale : (float)(1.0 / sqrt((double)s->d));
   a.cap = s->softcap;
+  a.inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
   if (m != nullptr) a.mask = *m;
   a.qs = canonical(s->q, s->B, s->Hq, s->Sq, s->d);
   a.ks = canonical(s->k, s->B, s->Hkv, s->Sk, s->d);
@@ -117,9 +119,8 @@ DenseArgs dense_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
 }
 
 // Keys are split over CTAs when the row tiles alone leave the GPU's 148 SMs (two CTAs each) mostly
-// idle and each split still has a few blocks of keys to work on.
+// idle and each split still has `least_keys` to work on.
 constexpr int kSlots = 2 * 148;
-constexpr int kMinSplitKeys = 256;
 constexpr int kMostCluster = 8;
 void split_in(DenseArgs& a, int64_t n) {
   const int64_t blocks = ((int64_t)a.Sk + kBlock - 1) / kBlock;
@@ -127,10 +128,10 @@ void split_in(DenseArgs& a, int64_t n) {
   a.split_keys = (int)(per * kBlock);
   a.splits = (int)((blocks + per - 1) / per);
 }
-void plan_splits(DenseArgs& a, int tile_rows_queries) {
+void plan_splits(DenseArgs& a, int tile_rows_queries, int least_keys) {
   const int64_t tiles = ((int64_t)a.Sq + tile_rows_queries - 1) / tile_rows_queries * a.Hkv * a.B;
   if (tiles * 2 <= kSlots) {
-    const int64_t most = ((int64_t)a.Sk + kMinSplitKeys - 1) / kMinSplitKeys;
+    const int64_t most = ((int64_t)a.Sk + least_keys - 1) / least_keys;
     split_in(a, imax<int64_t>(1, imin(kSlots / tiles, most)));
   }
   a.parts = a.splits;
@@ -147,7 +148,7 @@ void plan_few(DenseArgs& a) {
   a.parts = a.splits / a.cluster;
 }
 bool few_rows(const DenseArgs& a, int dtype) {
-  return dtype == FVATTN_BF16 && (int64_t)a.Sq * a.G <= kFewRows && (int64_t)a.B * a.Hkv <= 65535;
+  return dtype == FVATTN_BF16 && (int64_t)a.Sq * a.G <= kFewRows;
 }
 
 size_t take(size_t& off, size_t bytes) {
@@ -193,8 +194,10 @@ DenseArgs fwd_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
   DenseArgs a = dense_args(s, m);
   if (few_rows(a, s->dtype))
     plan_few(a);
+  else if (s->dtype == FVATTN_F32)
+    plan_splits(a, imax(1, 64 / a.G), kBlock);         // a tile of 64 keys takes it several microseconds
   else
-    plan_splits(a, s->dtype == FVATTN_F32 ? imax(1, 64 / a.G) : kTileRows / a.G);
+    plan_splits(a, kTileRows / a.G, 256);
   return a;
 }
 

@@ -25,7 +25,7 @@ struct DenseArgs {
   fvattn_dense_mask mask;
   int B, Hq, Hkv, G, Sq, Sk, d;
   int causal;
-  float scale, cap;
+  float scale, cap, inv_cap;
   int splits, split_keys;         // forward: the keys in `splits` ranges of split_keys (a multiple of 64)
   int cluster, parts;             // ranges joined within a cluster; what is left to join through memory
   float *part_o, *part_lse;       // parts > 1: [parts][B][Hq][Sq][d] and [parts][B][Hq][Sq]

@@ -28,12 +28,6 @@ __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xffff0000u));
-}
-
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   const float4 a = load4(p), b = load4(p + 4);
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
@@ -58,21 +52,21 @@ struct Tile {
 };
 
 // Rows row0.. of a key head's (query, head of the group) rows into shared memory; others as zeros.
-template <typename T, int D>
-__device__ __forceinline__ void load_rows(float* dst, const T* base, const fvattn_strides& st, int b, int h0, int G,
-                                          int64_t row0, int64_t nrows) {
+template <int D>
+__device__ __forceinline__ void load_rows(float* dst, const float* base, const fvattn_strides& st, int b, int h0, int G,
+                                          int row0, int nrows) {
   for (int x = threadIdx.x; x < kT * (D / 4); x += kThreads) {
     const int r = x / (D / 4), c = (x % (D / 4)) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t rho = row0 + r;
-    if (rho < nrows) v = load4(base + b * st.b + (h0 + rho % G) * st.h + (rho / G) * st.s + c);
+    const int rho = row0 + r;
+    if (rho < nrows) v = load4(base + b * st.b + (h0 + rho % G) * st.h + (int64_t)(rho / G) * st.s + c);
     *reinterpret_cast<float4*>(dst + r * Tile<D>::kLd + c) = v;
   }
 }
 
 // Keys j0.. below `end` of one key head; others as zeros (whatever they hold). Padding keys too.
-template <typename T, int D>
-__device__ __forceinline__ void load_keys(float* dst, const T* base, const fvattn_strides& st, int b, int h, int j0,
+template <int D>
+__device__ __forceinline__ void load_keys(float* dst, const float* base, const fvattn_strides& st, int b, int h, int j0,
                                           int end, const int32_t* doc) {
   for (int x = threadIdx.x; x < kT * (D / 4); x += kThreads) {
     const int r = x / (D / 4), c = (x % (D / 4)) * 4;
@@ -83,55 +77,90 @@ __device__ __forceinline__ void load_keys(float* dst, const T* base, const fvatt
   }
 }
 
-// acc[i][j] = A[ty*4 + i] . B[tx + 16 j] over D.
+// Pairs of fp32 (one 64-bit register): two products per instruction, and shared memory gives them as
+// they are.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
+// acc[i][j] = A[ty*4 + i] . B[tx + 16 j] over D (even and odd elements apart until the end).
 template <int D>
 __device__ __forceinline__ void dot_tile(const float* A, const float* B, int ty, int tx, float (&acc)[4][4]) {
   constexpr int LD = Tile<D>::kLd;
+  uint64_t sum[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) sum[i][j] = 0ull;
 #pragma unroll 4
   for (int c = 0; c < D; c += 4) {
-    float4 x[4], y[4];
+    ulonglong2 x[4], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(A + (ty * 4 + i) * LD + c);
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(A + (ty * 4 + i) * LD + c);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * LD + c);
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * j) * LD + c);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-        acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-        acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-        acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
-      }
+      for (int j = 0; j < 4; ++j) sum[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, sum[i][j]));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 v = both(sum[i][j]);
+      acc[i][j] = v.x + v.y;
+    }
 }
 
-// acc[i][:] += sum_j W[ty*4 + i][j] X[j][tx*4 + 64 c ..] over the 64 j of a tile.
+// acc[i] (pairs of columns tx*4 + 64 c ..) += sum_j W[ty*4 + i][j] X[j] over the 64 j of a tile.
 template <int D>
-__device__ __forceinline__ void add_product(const float* W, const float* X, int ty, int tx, float (&acc)[4][D / 16]) {
+__device__ __forceinline__ void add_product(const float* W, const float* X, int ty, int tx, uint64_t (&acc)[4][D / 32]) {
 #pragma unroll 2
   for (int j = 0; j < kT; j += 4) {
     float4 w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty * 4 + i) * Tile<D>::kLdP + j);
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj)
+    for (int jj = 0; jj < 4; ++jj) {
+      uint64_t ww[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
+        ww[i] = pair(v, v);
+      }
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        const float4 x = *reinterpret_cast<const float4*>(X + (j + jj) * Tile<D>::kLd + tx * 4 + 64 * c);
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(X + (j + jj) * Tile<D>::kLd + tx * 4 + 64 * c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float wi = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
-          acc[i][4 * c] = fmaf(wi, x.x, acc[i][4 * c]);
-          acc[i][4 * c + 1] = fmaf(wi, x.y, acc[i][4 * c + 1]);
-          acc[i][4 * c + 2] = fmaf(wi, x.z, acc[i][4 * c + 2]);
-          acc[i][4 * c + 3] = fmaf(wi, x.w, acc[i][4 * c + 3]);
+          acc[i][2 * c] = fma2(ww[i], x.x, acc[i][2 * c]);
+          acc[i][2 * c + 1] = fma2(ww[i], x.y, acc[i][2 * c + 1]);
         }
       }
+    }
+  }
+}
+
+// Times `by`, to the columns of a row.
+template <int D>
+__device__ __forceinline__ void store_cols(float* p, int tx, const uint64_t (&acc)[D / 32], float by) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    const float2 x = both(acc[2 * c]), y = both(acc[2 * c + 1]);
+    *reinterpret_cast<float4*>(p + tx * 4 + 64 * c) = make_float4(x.x * by, x.y * by, y.x * by, y.y * by);
   }
 }
 
@@ -140,7 +169,7 @@ __device__ __forceinline__ float score(const DenseArgs& a, const DenseRow& r, fl
   float s = x * a.scale;
   *slope_of_cap = 1.f;
   if (a.cap > 0.f) {
-    const float t = tanhf(s / a.cap);
+    const float t = tanhf(s * a.inv_cap);
     s = a.cap * t;
     *slope_of_cap = 1.f - t * t;
   }
@@ -159,42 +188,77 @@ __device__ __forceinline__ float half_warp_sum(float v) {
   return v;
 }
 
-// grid: (row tiles * splits, Hkv, B)
-template <typename T, int D>
+// Keys j0.. below `end` as load_keys, by asynchronous copies.
+template <int D>
+__device__ __forceinline__ void copy_keys_async(float* dst, const float* base, const fvattn_strides& st, int b, int h, int j0,
+                                                int end, const int32_t* doc) {
+  for (int x = threadIdx.x; x < kT * (D / 4); x += kThreads) {
+    const int r = x / (D / 4), c = (x % (D / 4)) * 4, j = j0 + r;
+    const bool take = j < end && (doc == nullptr || doc[j] >= 0);
+    const float* src = base + b * st.b + h * st.h + (take ? (int64_t)j * st.s + c : 0);
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * Tile<D>::kLd + c));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(take ? 16 : 0) : "memory");
+  }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// grid: (row tiles * splits, Hkv, B). The next tile's keys are copied while this one's are worked on; warps
+// whose rows are all past the last one (few queries) only copy.
+template <int D>
 __global__ void __launch_bounds__(kThreads) dense_fwd_kernel(const DenseArgs a) {
   allow_next_grid();
   extern __shared__ float sm[];
-  float *sQ = sm, *sK = sQ + Tile<D>::kFloats, *sV = sK + Tile<D>::kFloats, *sP = sV + Tile<D>::kFloats;
+  float *sQ = sm, *sKV = sQ + Tile<D>::kFloats, *sP = sKV + 4 * Tile<D>::kFloats;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int split = blockIdx.x % a.splits, tile = gridDim.x / a.splits - 1 - blockIdx.x / a.splits;
   const int h = blockIdx.y, b = blockIdx.z, h0 = h * a.G;
-  const int64_t nrows = (int64_t)a.Sq * a.G, row0 = (int64_t)tile * kT;
+  const int nrows = a.Sq * a.G, row0 = tile * kT;
   const DenseSeq seq = dense_seq(a, b);
   const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
-  load_rows<T, D>(sQ, static_cast<const T*>(a.q), a.qs, b, h0, a.G, row0, nrows);
+  const int last = min(row0 + kT, nrows) - 1;
+  const int begin = split * a.split_keys;
+  const int end = (int)imin<int64_t>(dense_limit(seq, a.causal, last / a.G), (int64_t)begin + a.split_keys);
+  auto copy = [&](int j0, int buf) {
+    float* to = sKV + buf * 2 * Tile<D>::kFloats;
+    copy_keys_async<D>(to, static_cast<const float*>(a.k), a.ks, b, h, j0, end, doc_k);
+    copy_keys_async<D>(to + Tile<D>::kFloats, static_cast<const float*>(a.v), a.vs, b, h, j0, end, doc_k);
+    copies_commit();
+  };
+  if (begin < end) copy(begin, 0);
+  load_rows<D>(sQ, static_cast<const float*>(a.q), a.qs, b, h0, a.G, row0, nrows);
 
   DenseRow row[4];
-  float mx[4], l[4], o[4][D / 16];
+  float mx[4], l[4];
+  uint64_t o[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t rho = row0 + ty * 4 + i;
+    const int rho = row0 + ty * 4 + i;
     if (rho < nrows)
-      row[i] = dense_row(a, seq, b, h0 + (int)(rho % a.G), (int)(rho / a.G));
+      row[i] = dense_row(a, seq, b, h0 + rho % a.G, rho / a.G);
     else
       row[i] = DenseRow{0, 0, 0, 0.f};
     mx[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    for (int c = 0; c < D / 32; ++c) o[i][c] = 0ull;
   }
-  const int64_t last = imin<int64_t>(row0 + kT, nrows) - 1;
-  const int begin = split * a.split_keys;
-  const int end = (int)imin<int64_t>(dense_limit(seq, a.causal, (int)(last / a.G)), (int64_t)begin + a.split_keys);
-  for (int j0 = begin; j0 < end; j0 += kT) {
+  const bool live = row0 + (threadIdx.x >> 5) * 8 < nrows;       // the same for a warp
+  int buf = 0;
+  for (int j0 = begin; j0 < end; j0 += kT, buf ^= 1) {
+    __syncthreads();                     // the buffer that the next copies fill has been read
+    if (j0 + kT < end) {
+      copy(j0 + kT, buf ^ 1);
+      copies_wait<1>();
+    } else {
+      copies_wait<0>();
+    }
     __syncthreads();
-    load_keys<T, D>(sK, static_cast<const T*>(a.k), a.ks, b, h, j0, end, doc_k);
-    load_keys<T, D>(sV, static_cast<const T*>(a.v), a.vs, b, h, j0, end, doc_k);
-    __syncthreads();
+    if (!live) continue;
+    const float *sK = sKV + buf * 2 * Tile<D>::kFloats, *sV = sK + Tile<D>::kFloats;
     float s[4][4];
     dot_tile<D>(sQ, sK, ty, tx, s);
 #pragma unroll
@@ -221,35 +285,28 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_kernel(const DenseArgs a) 
       l[i] = l[i] * f + half_warp_sum(add);
       mx[i] = mn;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
+      for (int c = 0; c < D / 32; ++c) o[i][c] = fma2(o[i][c], pair(f, f), 0ull);
     }
     __syncwarp();                // a row's weights are written and read by one half warp
     add_product<D>(sP, sV, ty, tx, o);
+    __syncwarp();
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t rho = row0 + ty * 4 + i;
+    const int rho = row0 + ty * 4 + i;
     if (rho >= nrows) continue;
-    const int hq = h0 + (int)(rho % a.G);
+    const int hq = h0 + rho % a.G;
     const int64_t iq = rho / a.G, flat = ((int64_t)b * a.Hq + hq) * a.Sq + iq;
     const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
     const float lse = l[i] == 0.f ? -INFINITY : mx[i] + logf(l[i]);
-    if (a.splits > 1) {
-      const int64_t at = (int64_t)split * a.B * a.Hq * a.Sq + flat;
-      float* p = a.part_o + at * D;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) p[tx * 4 + 64 * (c / 4) + c % 4] = o[i][c] * inv;
-      if (tx == 0) a.part_lse[at] = lse;
-    } else {
-      T* p = static_cast<T*>(a.out) + b * a.os.b + hq * a.os.h + iq * a.os.s;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const int at = tx * 4 + 64 * (c / 4) + c % 4;
-        const float x = o[i][c] * inv;
-        put(p + at, x);
-        if (a.rest != nullptr) put(static_cast<T*>(a.rest) + (p - static_cast<T*>(a.out)) + at, x - to_f32(p[at]));
-      }
-      if (tx == 0 && a.lse != nullptr) a.lse[flat] = lse;
+    const int64_t at = (int64_t)split * a.B * a.Hq * a.Sq + flat;
+    float* p = a.parts > 1 ? a.part_o + at * D : static_cast<float*>(a.out) + b * a.os.b + hq * a.os.h + iq * a.os.s;
+    store_cols<D>(p, tx, o[i], inv);
+    if (tx == 0) {
+      if (a.parts > 1)
+        a.part_lse[at] = lse;
+      else if (a.lse != nullptr)
+        a.lse[flat] = lse;
     }
   }
 }
@@ -377,41 +434,42 @@ __device__ __forceinline__ void pair_grads(const DenseArgs& a, const DenseRow& r
 }
 
 // grid: (row tiles, Hkv, B)
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) dense_dq_kernel(const DenseArgs a) {
   extern __shared__ float sm[];
   float *sQ = sm, *sG = sQ + Tile<D>::kFloats, *sK = sG + Tile<D>::kFloats, *sV = sK + Tile<D>::kFloats,
         *sP = sV + Tile<D>::kFloats;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int tile = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z, h0 = h * a.G;
-  const int64_t nrows = (int64_t)a.Sq * a.G, row0 = (int64_t)tile * kT;
+  const int nrows = a.Sq * a.G, row0 = tile * kT;
   const DenseSeq seq = dense_seq(a, b);
   const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
-  load_rows<T, D>(sQ, static_cast<const T*>(a.q), a.qs, b, h0, a.G, row0, nrows);
-  load_rows<T, D>(sG, static_cast<const T*>(a.dout), a.dos, b, h0, a.G, row0, nrows);
+  load_rows<D>(sQ, static_cast<const float*>(a.q), a.qs, b, h0, a.G, row0, nrows);
+  load_rows<D>(sG, static_cast<const float*>(a.dout), a.dos, b, h0, a.G, row0, nrows);
   DenseRow row[4];
-  float lse[4], delta[4], dq[4][D / 16];
+  float lse[4], delta[4];
+  uint64_t dq[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t rho = row0 + ty * 4 + i;
+    const int rho = row0 + ty * 4 + i;
     row[i] = DenseRow{0, 0, 0, 0.f};
     lse[i] = delta[i] = 0.f;
     if (rho < nrows) {
-      const int hq = h0 + (int)(rho % a.G);
+      const int hq = h0 + rho % a.G;
       const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + rho / a.G;
-      row[i] = dense_row(a, seq, b, hq, (int)(rho / a.G));
+      row[i] = dense_row(a, seq, b, hq, rho / a.G);
       lse[i] = a.lse[flat];
       delta[i] = a.delta[flat];
     }
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) dq[i][c] = 0.f;
+    for (int c = 0; c < D / 32; ++c) dq[i][c] = 0ull;
   }
-  const int64_t last = imin<int64_t>(row0 + kT, nrows) - 1;
-  const int end = dense_limit(seq, a.causal, (int)(last / a.G));
+  const int last = min(row0 + kT, nrows) - 1;
+  const int end = dense_limit(seq, a.causal, last / a.G);
   for (int j0 = 0; j0 < end; j0 += kT) {
     __syncthreads();
-    load_keys<T, D>(sK, static_cast<const T*>(a.k), a.ks, b, h, j0, end, doc_k);
-    load_keys<T, D>(sV, static_cast<const T*>(a.v), a.vs, b, h, j0, end, doc_k);
+    load_keys<D>(sK, static_cast<const float*>(a.k), a.ks, b, h, j0, end, doc_k);
+    load_keys<D>(sV, static_cast<const float*>(a.v), a.vs, b, h, j0, end, doc_k);
     __syncthreads();
     float s[4][4], dp[4][4];
     dot_tile<D>(sQ, sK, ty, tx, s);
@@ -429,38 +487,37 @@ __global__ void __launch_bounds__(kThreads) dense_dq_kernel(const DenseArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t rho = row0 + ty * 4 + i;
+    const int rho = row0 + ty * 4 + i;
     if (rho >= nrows) continue;
-    T* p = static_cast<T*>(a.dq) + b * a.dqs.b + (h0 + rho % a.G) * a.dqs.h + (rho / a.G) * a.dqs.s;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) put(p + tx * 4 + 64 * (c / 4) + c % 4, dq[i][c]);
+    float* p = static_cast<float*>(a.dq) + b * a.dqs.b + (h0 + rho % a.G) * a.dqs.h + (int64_t)(rho / a.G) * a.dqs.s;
+    store_cols<D>(p, tx, dq[i], 1.f);
   }
 }
 
 // grid: (key tiles, Hkv, B)
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) dense_dkv_kernel(const DenseArgs a) {
   extern __shared__ float sm[];
   float *sK = sm, *sV = sK + Tile<D>::kFloats, *sQ = sV + Tile<D>::kFloats, *sG = sQ + Tile<D>::kFloats,
         *sP = sG + Tile<D>::kFloats, *sS = sP + Tile<D>::kFloatsP;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int j0 = blockIdx.x * kT, h = blockIdx.y, b = blockIdx.z, h0 = h * a.G;
-  const int64_t nrows = (int64_t)a.Sq * a.G;
+  const int nrows = a.Sq * a.G;
   const DenseSeq seq = dense_seq(a, b);
   const int32_t* doc_k = a.mask.doc_k != nullptr ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
-  load_keys<T, D>(sK, static_cast<const T*>(a.k), a.ks, b, h, j0, seq.kv, doc_k);
-  load_keys<T, D>(sV, static_cast<const T*>(a.v), a.vs, b, h, j0, seq.kv, doc_k);
-  float dk[4][D / 16], dv[4][D / 16];
+  load_keys<D>(sK, static_cast<const float*>(a.k), a.ks, b, h, j0, seq.kv, doc_k);
+  load_keys<D>(sV, static_cast<const float*>(a.v), a.vs, b, h, j0, seq.kv, doc_k);
+  uint64_t dk[4][D / 32], dv[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
-  for (int64_t row0 = 0; row0 < nrows; row0 += kT) {
-    const int64_t last = imin<int64_t>(row0 + kT, nrows) - 1;
-    if (dense_limit(seq, a.causal, (int)(last / a.G)) <= j0) continue;    // the same for the whole CTA
+    for (int c = 0; c < D / 32; ++c) dk[i][c] = dv[i][c] = 0ull;
+  for (int row0 = 0; row0 < nrows; row0 += kT) {
+    const int last = min(row0 + kT, nrows) - 1;
+    if (dense_limit(seq, a.causal, last / a.G) <= j0) continue;    // the same for the whole CTA
     __syncthreads();
-    load_rows<T, D>(sQ, static_cast<const T*>(a.q), a.qs, b, h0, a.G, row0, nrows);
-    load_rows<T, D>(sG, static_cast<const T*>(a.dout), a.dos, b, h0, a.G, row0, nrows);
+    load_rows<D>(sQ, static_cast<const float*>(a.q), a.qs, b, h0, a.G, row0, nrows);
+    load_rows<D>(sG, static_cast<const float*>(a.dout), a.dos, b, h0, a.G, row0, nrows);
     __syncthreads();
     // scores as [key][row]: this thread's four keys, four rows
     float s[4][4], dp[4][4];
@@ -468,13 +525,13 @@ __global__ void __launch_bounds__(kThreads) dense_dkv_kernel(const DenseArgs a) 
     dot_tile<D>(sV, sG, ty, tx, dp);
 #pragma unroll
     for (int rr = 0; rr < 4; ++rr) {
-      const int64_t rho = row0 + tx + 16 * rr;
+      const int rho = row0 + tx + 16 * rr;
       DenseRow row{0, 0, 0, 0.f};
       float lse = 0.f, delta = 0.f;
       if (rho < nrows) {
-        const int hq = h0 + (int)(rho % a.G);
+        const int hq = h0 + rho % a.G;
         const int64_t flat = ((int64_t)b * a.Hq + hq) * a.Sq + rho / a.G;
-        row = dense_row(a, seq, b, hq, (int)(rho / a.G));
+        row = dense_row(a, seq, b, hq, rho / a.G);
         lse = a.lse[flat];
         delta = a.delta[flat];
       }
@@ -490,7 +547,7 @@ __global__ void __launch_bounds__(kThreads) dense_dkv_kernel(const DenseArgs a) 
     if (a.mask.doc_q != nullptr) {
       __syncthreads();
       for (int r = threadIdx.x; r < kT; r += kThreads) {
-        const int64_t rho = row0 + r;
+        const int rho = row0 + r;
         if (rho < nrows && a.mask.doc_q[(int64_t)b * a.Sq + rho / a.G] < 0)
           for (int c = 0; c < D; ++c) sQ[r * Tile<D>::kLd + c] = sG[r * Tile<D>::kLd + c] = 0.f;
       }
@@ -505,13 +562,10 @@ __global__ void __launch_bounds__(kThreads) dense_dkv_kernel(const DenseArgs a) 
   for (int i = 0; i < 4; ++i) {
     const int j = j0 + ty * 4 + i;
     if (j >= a.Sk) continue;
-    T* pk = static_cast<T*>(a.dk) + b * a.dks.b + h * a.dks.h + (int64_t)j * a.dks.s;
-    T* pv = static_cast<T*>(a.dv) + b * a.dvs.b + h * a.dvs.h + (int64_t)j * a.dvs.s;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      put(pk + tx * 4 + 64 * (c / 4) + c % 4, dk[i][c]);
-      put(pv + tx * 4 + 64 * (c / 4) + c % 4, dv[i][c]);
-    }
+    float* pk = static_cast<float*>(a.dk) + b * a.dks.b + h * a.dks.h + (int64_t)j * a.dks.s;
+    float* pv = static_cast<float*>(a.dv) + b * a.dvs.b + h * a.dvs.h + (int64_t)j * a.dvs.s;
+    store_cols<D>(pk, tx, dk[i], 1.f);
+    store_cols<D>(pv, tx, dv[i], 1.f);
   }
 }
 
@@ -525,18 +579,18 @@ cudaError_t run(K kernel, dim3 grid, size_t smem, const DenseArgs& a, cudaStream
 
 unsigned row_tiles(const DenseArgs& a) { return (unsigned)(((int64_t)a.Sq * a.G + kT - 1) / kT); }
 
-template <typename T, int D>
+template <int D>
 cudaError_t fwd_d(const DenseArgs& a, cudaStream_t st) {
-  const size_t smem = (3 * Tile<D>::kFloats + Tile<D>::kFloatsP) * sizeof(float);
-  return run(dense_fwd_kernel<T, D>, dim3(row_tiles(a) * a.splits, a.Hkv, a.B), smem, a, st);
+  const size_t smem = (5 * Tile<D>::kFloats + Tile<D>::kFloatsP) * sizeof(float);
+  return run(dense_fwd_kernel<D>, dim3(row_tiles(a) * a.splits, a.Hkv, a.B), smem, a, st);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t bwd_d(const DenseArgs& a, cudaStream_t st) {
   const size_t smem = (4 * Tile<D>::kFloats + 2 * Tile<D>::kFloatsP) * sizeof(float);
-  const cudaError_t e = run(dense_dq_kernel<T, D>, dim3(row_tiles(a), a.Hkv, a.B), smem, a, st);
+  const cudaError_t e = run(dense_dq_kernel<D>, dim3(row_tiles(a), a.Hkv, a.B), smem, a, st);
   if (e != cudaSuccess) return e;
-  return run(dense_dkv_kernel<T, D>, dim3((unsigned)((a.Sk + kT - 1) / kT), a.Hkv, a.B), smem, a, st);
+  return run(dense_dkv_kernel<D>, dim3((unsigned)((a.Sk + kT - 1) / kT), a.Hkv, a.B), smem, a, st);
 }
 
 unsigned warp_rows(const DenseArgs& a) {
@@ -546,10 +600,10 @@ unsigned warp_rows(const DenseArgs& a) {
 }  // namespace
 
 cudaError_t launch_dense_f32(const DenseArgs& a, cudaStream_t st) {
-  return a.d == 128 ? fwd_d<float, 128>(a, st) : fwd_d<float, 64>(a, st);
+  return a.d == 128 ? fwd_d<128>(a, st) : fwd_d<64>(a, st);
 }
 cudaError_t launch_dense_f32_bwd(const DenseArgs& a, cudaStream_t st) {
-  return a.d == 128 ? bwd_d<float, 128>(a, st) : bwd_d<float, 64>(a, st);
+  return a.d == 128 ? bwd_d<128>(a, st) : bwd_d<64>(a, st);
 }
 cudaError_t launch_dense_prepare(const DenseArgs& a, int dtype, cudaStream_t st) {
   auto warps = [](int64_t B, int64_t S, int64_t size) {

@@ -421,9 +421,9 @@ int fvattn_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, const
 /*
  * Attention over all keys.
  *  B, Hq, Hkv, Sq, Sk, d  Hq a multiple of Hkv, at most 64 times it (query head h reads key head
- *                    h / (Hq / Hkv)); Sq and Sk independent, >= 1; d 64 or 128.
+ *                    h / (Hq / Hkv)); B * Hkv at most 65535; Sq and Sk independent, >= 1; d 64 or 128.
  *  dtype             fvattn_dtype. scale: <= 0 means 1/sqrt(d).
- *  softcap           0, or c > 0: scores become c tanh(score / c).
+ *  softcap           0, or c in [1e-20, 1e20]: scores become c tanh(score / c).
  *  causal            1: key j is visible to the query at position p when j <= p, or when
  *                    j < prefix_len of its sequence.
  *  q, k, v, o        strides of q, k, v and out (rest has out's); dout, dq, dk, dv: the gradients'.

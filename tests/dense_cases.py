@@ -108,6 +108,6 @@ def compare(got, r, b):
         assert a.shape == want.shape, n
         gone = ~np.isfinite(want)
         np.testing.assert_array_equal(a[gone], want[gone], err_msg=n)
-        far = np.abs(a - want)[~gone] / b[n][~gone]
+        far = np.abs(a[~gone] - want[~gone]) / b[n][~gone]
         assert not np.isnan(far).any(), f"{n}: NaN"
         assert far.max(initial=0.0) <= 1.0, f"{n}: {far.max():.2f} times its bound"

@@ -83,8 +83,9 @@ def call_bwd(lib, s, m=None, dout=P, q=P, k=P, v=P, out=P, rest=None, lse=P, dq=
 BAD = [(dict(B=0), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID), (dict(Sq=0), INVALID), (dict(Sk=0), INVALID),
        (dict(Hq=5), INVALID), (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED), (dict(dtype=3), INVALID),
        (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(softcap=-1.0), INVALID),
-       (dict(softcap=float("nan")), INVALID), (dict(softcap=float("inf")), INVALID), (dict(causal=2), INVALID),
-       (dict(Hq=130, Hkv=2), UNSUPPORTED), (dict(B=70000), UNSUPPORTED), (dict(Sk=1 << 30), UNSUPPORTED),
+       (dict(softcap=float("nan")), INVALID), (dict(softcap=float("inf")), INVALID),
+       (dict(softcap=1e-30), INVALID), (dict(softcap=1e30), INVALID), (dict(causal=2), INVALID),
+       (dict(Hq=130, Hkv=2), UNSUPPORTED), (dict(B=70000), UNSUPPORTED), (dict(B=40000), UNSUPPORTED), (dict(Sk=1 << 30), UNSUPPORTED),
        (dict(q=st(2560, 0, 64)), INVALID), (dict(k=st(2560, 1280, 60)), INVALID), (dict(v=st(0, 1280, 64)), INVALID),
        (dict(o=st(-2560, 640, 64)), INVALID)]
 

@@ -139,6 +139,25 @@ def test_few_queries_over_many_keys(dtype, shape):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 25.0])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("docs", [False, True])
+def test_all_together(dtype, d, cap, bias, docs):
+    # every combination of the kernels' variants, for whole sequences and for one to eight queries (up to
+    # 16, 24 and 32 rows of a shared key head)
+    for B, Hq, Hkv, Sq, Sk in ((2, 4, 2, 190, 190), (2, 6, 2, 1, 300), (1, 16, 1, 1, 700), (2, 8, 2, 4, 333),
+                               (1, 8, 1, 3, 500), (1, 4, 1, 8, 270)):
+        doc_k = documents(B, Sk, 60, pad=9, seed=4) if docs else None
+        doc_q = doc_k[:, Sk - Sq:].contiguous() if docs else None
+        if docs and Sq > 1:
+            doc_q[:, -1] = doc_q[:, 0]
+        cfg = fv.AttnConfig(causal=True, softcap=cap, slopes=slopes(Hq) if bias else None, doc_q=doc_q, doc_k=doc_k,
+                            prefix_len=i32(*[11 * b for b in range(B)]), kv_len=i32(*[Sk - 5 * b for b in range(B)]))
+        check((B, Hq, Hkv, Sq, Sk, d), dtype, cfg, seed=Sq, spread=2.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_strides(dtype):
     # slices of one [B, S, H, d] projection, a place in a longer cache, transposed outputs
     B, Hq, Hkv, S, d = 2, 4, 2, 140, 64
