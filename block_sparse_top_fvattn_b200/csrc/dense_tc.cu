@@ -38,6 +38,7 @@ namespace {
 constexpr int NS = 2;          // stages of K and of V; the stage of a step is also its S / P buffer
 constexpr int kWarps = 6;      // loader, MMA, four softmax warps
 constexpr float kRescaleLog2 = 8.0f;
+constexpr float kBoundedCap = 64.0f;      // e^64 times 2^20 keys of values up to 2^14 is in fp32's range
 
 template <int D>
 struct FwdLayout {
@@ -269,7 +270,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     const bool live_warp = __any_sync(0xffffffffu, valid);
     const int32_t* doc_k = DOCS ? a.mask.doc_k + (int64_t)b * a.Sk : nullptr;
     const ScoreMap<CAP, BIAS> map(a, row);
-    float mrow = -INFINITY;
+    // Capped scores need no maximum: their exponentials lie between e^-cap and e^cap.
+    const bool bounded = CAP && !BIAS && a.cap <= kBoundedCap;
+    float mrow = bounded ? 0.f : -INFINITY;
     uint64_t lsum = f2(0.f, 0.f);
     uint32_t g = 0;
     bool ok = true;
@@ -297,34 +300,36 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             if (!(((uint32_t)(see >> 32) >> c) & 1u)) hi[c] = __float_as_uint(-INFINITY);
           }
         }
-        const float mx = fmaxf(max32(lo), max32(hi)) * map.after;
-        const bool raise = mrow == -INFINITY || mx > mrow + kRescaleLog2;
-        const bool scale_o = raise && g > 0 && mrow != -INFINITY;
-        if (__any_sync(0xffffffffu, scale_o)) {
-          // tcgen05.ld/st are warp-collective: each lane with its own factor (1 where the max stays)
-          const uint32_t gp = g - 1;
-          if (!warp_wait(&bars->pv_done[gp & 1], (gp >> 1) & 1, abort)) {
-            fail(&bars->abort, 12);
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-          const float alpha = scale_o ? ex2(mrow - mx) : 1.f;
+        if (!bounded) {
+          const float mx = fmaxf(max32(lo), max32(hi)) * map.after;
+          const bool raise = mrow == -INFINITY || mx > mrow + kRescaleLog2;
+          const bool scale_o = raise && g > 0 && mrow != -INFINITY;
+          if (__any_sync(0xffffffffu, scale_o)) {
+            // tcgen05.ld/st are warp-collective: each lane with its own factor (1 where the max stays)
+            const uint32_t gp = g - 1;
+            if (!warp_wait(&bars->pv_done[gp & 1], (gp >> 1) & 1, abort)) {
+              fail(&bars->abort, 12);
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const float alpha = scale_o ? ex2(mrow - mx) : 1.f;
 #pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];
-            tc::tmem_ld32(tbase + lane_off + L::kColO + cc * 32, o);
-            tc::tmem_ld_wait();
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[32];
+              tc::tmem_ld32(tbase + lane_off + L::kColO + cc * 32, o);
+              tc::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st32(tbase + lane_off + L::kColO + cc * 32, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc::tmem_st32(tbase + lane_off + L::kColO + cc * 32, o);
+            }
+            tc::tmem_st_wait();
+            float l0, l1;
+            f2_split(lsum, l0, l1);
+            lsum = f2(l0 * alpha, l1 * alpha);
           }
-          tc::tmem_st_wait();
-          float l0, l1;
-          f2_split(lsum, l0, l1);
-          lsum = f2(l0 * alpha, l1 * alpha);
+          if (raise) mrow = mx;
         }
-        if (raise) mrow = mx;
         // a row that has seen nothing so far keeps -inf; its weights are exp2(-inf) = 0
         const float nm = mrow == -INFINITY ? 0.f : -mrow;
         const uint64_t negm = f2(nm, nm), after2 = f2(map.after, map.after);

@@ -189,18 +189,20 @@ __device__ __forceinline__ uint64_t visible64(const DenseRow& row, const int32_t
   return see;
 }
 
-// tanh on pairs, |y| <= 1: y times a polynomial of degree 6 in y^2, fitted to the least largest error
-// (2e-8; 1e-7 with fp32 arithmetic). On the FMA pipe: the exponentials of the softmax already fill the
-// SFU, and tanh by exponential and reciprocal would triple its work.
+// tanh on pairs: y times a polynomial in y^2, fitted to the least largest error (2e-8 either way; 1e-7
+// with fp32 arithmetic), of degree 4 for |y| <= 0.6 and 6 for |y| <= 1. On the FMA pipe: the
+// exponentials of the softmax already fill the SFU, and tanh by exponential and reciprocal would triple
+// its work.
+template <int DEGREE>
 __device__ __forceinline__ uint64_t tanh_small2(uint64_t y) {
+  constexpr float c4[5] = {0.9999996423721313f, -0.33331209421157837f, 0.13299210369586945f, -0.05169673636555672f,
+                           0.01497695129364729f};
+  constexpr float c6[7] = {0.9999997019767761f,    -0.33332130312919617f, 0.13319583237171173f, -0.05326582491397858f,
+                           0.01997326873242855f, -0.005951268598437309f, 0.0009637684561312199f};
   const uint64_t u = fmul2(y, y);
-  uint64_t p = f2(0.0009637684561312199f, 0.0009637684561312199f);
-  p = ffma2(p, u, f2(-0.005951268598437309f, -0.005951268598437309f));
-  p = ffma2(p, u, f2(0.01997326873242855f, 0.01997326873242855f));
-  p = ffma2(p, u, f2(-0.05326582491397858f, -0.05326582491397858f));
-  p = ffma2(p, u, f2(0.13319583237171173f, 0.13319583237171173f));
-  p = ffma2(p, u, f2(-0.33332130312919617f, -0.33332130312919617f));
-  p = ffma2(p, u, f2(0.9999997019767761f, 0.9999997019767761f));
+  uint64_t p = DEGREE == 4 ? f2(c4[4], c4[4]) : f2(c6[6], c6[6]);
+#pragma unroll
+  for (int k = DEGREE - 1; k >= 0; --k) p = ffma2(p, u, DEGREE == 4 ? f2(c4[k % 5], c4[k % 5]) : f2(c6[k], c6[k]));
   return fmul2(p, y);
 }
 // tanh(y) = 1 - 2 / (1 + e^2y) for any y, off by a few 2^-24; e^2y at inf or 0 gives 1 and -1.
@@ -215,17 +217,24 @@ __device__ __forceinline__ float abs_max32(const uint32_t (&s)[32]) {
   return m;
 }
 
-// s <- tanh(s * in), the polynomial where every score of the warp allows it. The whole warp takes part.
-__device__ __forceinline__ void tanh32(uint32_t (&s)[32], float in) {
-  if (__all_sync(0xffffffffu, abs_max32(s) * in <= 1.f)) {
-    const uint64_t in2 = f2(in, in);
+template <int DEGREE>
+__device__ __forceinline__ void tanh32_small(uint32_t (&s)[32], float in) {
+  const uint64_t in2 = f2(in, in);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      float a, b;
-      f2_split(tanh_small2(fmul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), in2)), a, b);
-      s[c] = __float_as_uint(a);
-      s[c + 1] = __float_as_uint(b);
-    }
+  for (int c = 0; c < 32; c += 2) {
+    float a, b;
+    f2_split(tanh_small2<DEGREE>(fmul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), in2)), a, b);
+    s[c] = __float_as_uint(a);
+    s[c + 1] = __float_as_uint(b);
+  }
+}
+// s <- tanh(s * in), by the shortest form that every score of the warp allows. The whole warp takes part.
+__device__ __forceinline__ void tanh32(uint32_t (&s)[32], float in) {
+  const float top = abs_max32(s) * in;
+  if (__all_sync(0xffffffffu, top <= 0.6f)) {
+    tanh32_small<4>(s, in);
+  } else if (__all_sync(0xffffffffu, top <= 1.f)) {
+    tanh32_small<6>(s, in);
   } else {
 #pragma unroll
     for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(tanh_any(__uint_as_float(s[c]) * in));

@@ -60,7 +60,7 @@ def test_sizes(shape, dtype, causal):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("cap", [0.5, 5.0, 50.0])
+@pytest.mark.parametrize("cap", [0.5, 5.0, 50.0, 200.0])
 def test_softcap(dtype, d, cap):
     check((1, 4, 2, 150, 190, d), dtype, fv.AttnConfig(softcap=cap, causal=cap == 5.0), spread=3.0)
 
