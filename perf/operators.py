@@ -384,8 +384,8 @@ def _own_attn(st):
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     if not case["train"]:
         return {"out": fv.dense_attn(q, st["k"], st["v"], cfg, lse=lse), "lse": lse}
-    # a training step also keeps what the rounding of the output leaves, for the gradients
-    rest = torch.empty_like(q)
+    # a training step also keeps what the rounding of the output to bf16 leaves, for the gradients
+    rest = torch.empty_like(q) if q.dtype == torch.bfloat16 else None
     o = fv.dense_attn(q, st["k"], st["v"], cfg, lse=lse, rest=rest)
     dq, dk, dv = fv.dense_attn_bwd(st["g"], q, st["k"], st["v"], o, lse, cfg, rest=rest)
     return {"out": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
