@@ -9,7 +9,6 @@ positive multiples of 16 bytes (slices of a fused projection, places in a cache,
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 from typing import Optional, Tuple
@@ -17,7 +16,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from ._lib import FVATTN_BF16, FVATTN_F32, FvattnError, check, load
+from ._lib import FVATTN_BF16, FVATTN_F32, FVATTN_OK, FvattnError, load
 
 __all__ = ["qk_norm_rope", "qk_norm_rope_bwd", "AttnConfig", "dense_attn", "dense_attn_bwd"]
 
@@ -82,7 +81,8 @@ class _Plan:
     """A checked description of a call: the library's structures, the outputs it may have to make, scratch
     bytes."""
 
-    def __init__(self, shape, device, dtype, nws=0, out_shapes=()):
+    def __init__(self, name, shape, device, dtype, nws=0, out_shapes=()):
+        self.name, self.call, self.index = name, getattr(load(), name), device.index
         self.shape, self.ref, self.device, self.dtype, self.nws = shape, ctypes.byref(shape), device, dtype, nws
         self.outs = []
         for size in out_shapes:
@@ -91,15 +91,19 @@ class _Plan:
 
     def make(self, i: int, stream) -> torch.Tensor:
         """Output i, dense (the quickest of torch's ways to allocate a tensor)."""
-        return _made(torch.empty_strided(*self.outs[i], dtype=self.dtype, device=self.device), stream)
+        size, stride = self.outs[i]
+        t = torch.empty_strided(size, stride, dtype=self.dtype, device=self.device)
+        return t if stream is None else _made(t, stream)
 
-
-_HERE = contextlib.nullcontext()
-
-
-def _current(device: torch.device):
-    """Makes the device of a call current around its launches."""
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    def run(self, *args) -> None:
+        """The library's call, with the tensors' device current."""
+        if torch.cuda.current_device() == self.index:
+            code = self.call(*args)
+        else:
+            with torch.cuda.device(self.device):
+                code = self.call(*args)
+        if code != FVATTN_OK:
+            raise FvattnError(code, self.name)
 
 
 def _handle(device: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
@@ -200,7 +204,8 @@ def _qk_plan(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps, ou
         shp.dq, shp.dk = strides(grads, ("dq", "dk"), (q.shape, k.shape), True)
         if q_weight is not None:
             nws = int(load().fvattn_qk_norm_rope_workspace_bytes(ctypes.byref(shp)))
-    return _keep(key, _Plan(shp, q.device, q.dtype, nws, shapes if grads is None else (q.shape, k.shape)))
+    name = "fvattn_qk_norm_rope" if grads is None else "fvattn_qk_norm_rope_bwd"
+    return _keep(key, _Plan(name, shp, q.device, q.dtype, nws, shapes if grads is None else (q.shape, k.shape)))
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
@@ -224,10 +229,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
         q_out = plan.make(0, stream)
     if k_out is None:
         k_out = plan.make(1, stream)
-    with _current(plan.device):
-        check(load().fvattn_qk_norm_rope(q.data_ptr(), k.data_ptr(), plan.ref, _ptr(q_weight), _ptr(k_weight),
-                                         _ptr(cos), _ptr(sin), _ptr(positions), q_out.data_ptr(), k_out.data_ptr(),
-                                         _ptr(status), handle), "fvattn_qk_norm_rope")
+    plan.run(q.data_ptr(), k.data_ptr(), plan.ref, _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+             _ptr(positions), q_out.data_ptr(), k_out.data_ptr(), _ptr(status), handle)
     return q_out, k_out
 
 
@@ -252,11 +255,9 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
         dwq = _made(torch.empty(q.shape[3], dtype=torch.float32, device=plan.device), stream)
         dwk = _made(torch.empty(q.shape[3], dtype=torch.float32, device=plan.device), stream)
     ws = _scratch(plan, workspace, stream)
-    with _current(plan.device):
-        check(load().fvattn_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), plan.ref,
-                                             _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
-                                             dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), plan.nws,
-                                             _ptr(status), handle), "fvattn_qk_norm_rope_bwd")
+    plan.run(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), plan.ref, _ptr(q_weight), _ptr(k_weight),
+             _ptr(cos), _ptr(sin), _ptr(positions), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws),
+             plan.nws, _ptr(status), handle)
     return dq, dk, dwq, dwk
 
 
@@ -349,17 +350,18 @@ def _dense_plan(q, k, v, cfg: AttnConfig, scale, out, rest, lse, status, grads) 
         if q.dtype != torch.bfloat16 or (r.b, r.h, r.s) != (shp.o.b, shp.o.h, shp.o.s):
             raise ValueError("rest must be bf16 and have out's strides")
     lib = load()
+    name = "fvattn_dense_attn" if grads is None else "fvattn_dense_attn_bwd"
     mask = ctypes.byref(cfg.to_c())
     if grads is None:
         nws = int(lib.fvattn_dense_attn_workspace_bytes(ctypes.byref(shp), mask))
     else:
-        for name, t, like in zip(("dout", "dq", "dk", "dv"), grads, (q, q, k, v)):
-            setattr(shp, name, strides(t, name, like))
+        for n, t, like in zip(("dout", "dq", "dk", "dv"), grads, (q, q, k, v)):
+            setattr(shp, n, strides(t, n, like))
         nws = int(lib.fvattn_dense_attn_bwd_workspace_bytes(ctypes.byref(shp), mask))
     if nws == _lib.SIZE_ERROR:
         # the call that follows says what is wrong
-        return _Plan(shp, q.device, q.dtype, 0, (q.shape, k.shape, v.shape))
-    return _keep(key, _Plan(shp, q.device, q.dtype, nws, (q.shape, k.shape, v.shape)))
+        return _Plan(name, shp, q.device, q.dtype, 0, (q.shape, k.shape, v.shape))
+    return _keep(key, _Plan(name, shp, q.device, q.dtype, nws, (q.shape, k.shape, v.shape)))
 
 
 def dense_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cfg: Optional[AttnConfig] = None, *,
@@ -380,10 +382,8 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cfg: Optional[
     if out is None:
         out = plan.make(0, stream)
     ws = _scratch(plan, workspace, stream)
-    with _current(plan.device):
-        check(load().fvattn_dense_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()),
-                                       out.data_ptr(), _ptr(rest), _ptr(lse), _ptr(ws), plan.nws, _ptr(status), handle),
-              "fvattn_dense_attn")
+    plan.run(q.data_ptr(), k.data_ptr(), v.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()), out.data_ptr(), _ptr(rest),
+             _ptr(lse), _ptr(ws), plan.nws, _ptr(status), handle)
     return out
 
 
@@ -403,9 +403,7 @@ def dense_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     dk = plan.make(1, stream) if dk is None else dk
     dv = plan.make(2, stream) if dv is None else dv
     ws = _scratch(plan, workspace, stream)
-    with _current(plan.device):
-        check(load().fvattn_dense_attn_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                           _ptr(rest), lse.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()),
-                                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), plan.nws,
-                                           _ptr(status), handle), "fvattn_dense_attn_bwd")
+    plan.run(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(rest), lse.data_ptr(),
+             plan.ref, ctypes.byref(cfg.to_c()), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), plan.nws,
+             _ptr(status), handle)
     return dq, dk, dv
