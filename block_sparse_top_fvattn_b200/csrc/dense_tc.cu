@@ -19,6 +19,10 @@
 // With rest (the output to 16 bits, for the gradients) P goes in as two bf16 terms, the second of them
 // what the rounding of the first left, behind it in the S buffer, and the second product is made twice.
 //
+// Bound by the softmax warps, whose exponentials fill the SFU, then by the products. Measured, d = 128:
+// packed clips of 16380 tokens, 6 heads: 161 us, 622 TFLOP/s; prompts of 2 x 2047 tokens, 16 / 4 heads, capped:
+// 61 us; with rest, 8192 causal tokens, 12 heads: 232 us, tensor pipe 73 % active (186 us without rest).
+//
 // Every wait is bounded; one that runs out stops every role without leaving a copy or product in
 // flight, is reported in the status word, and makes the tile's rows NaN.
 #include <cuda.h>
@@ -38,7 +42,10 @@ namespace {
 constexpr int NS = 2;          // stages of K and of V; the stage of a step is also its S / P buffer
 constexpr int kWarps = 6;      // loader, MMA, four softmax warps
 constexpr float kRescaleLog2 = 8.0f;
-constexpr float kBoundedCap = 64.0f;      // e^64 times 2^20 keys of values up to 2^14 is in fp32's range
+// The largest cap whose scores are taken without a running maximum: e^50 < 2^73, so that 2^20 keys of values
+// up to 2^34 stay in fp32's range, and a row of scores at -cap sums to e^-50, a normal number. Capped rows of
+// 2047 tokens (prompts, 16 / 4 heads): 61 us without, 67 us with the maximum (and tanh to degree 6 throughout).
+constexpr float kBoundedCap = 50.0f;
 
 template <int D>
 struct FwdLayout {

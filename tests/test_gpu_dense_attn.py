@@ -272,6 +272,50 @@ def test_two_calls_at_once_on_two_streams():
             assert all(torch.equal(a[n], b[n]) for n in a)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cap", [30.0, 50.0, 50.5, 100.0])
+def test_saturated_caps_and_large_values(dtype, cap):
+    # every score at the cap or at its negative (scores of 25 times the cap: tanh is 1 to fp32), with and
+    # without a running maximum, and values whose sums times e^50 are 2^118
+    Sq, Sk, d = 130, 300, 64
+    x = draw(1, 2, 1, Sq, Sk, d, dtype)
+    sign = torch.ones(Sq, device="cuda")
+    sign[::2] = -1
+    x["q"] = (sign[:, None] * torch.ones(1, 2, Sq, d, device="cuda")).to(dtype)
+    x["k"] = torch.ones(1, 1, Sk, d, device="cuda").to(dtype)
+    x["v"] = x["v"] * 2.0 ** 34
+    cfg = fv.AttnConfig(softcap=cap)
+    got = run(x, cfg, grads=False, scale=25.0 * cap / d)
+    # equal scores: out is the mean of the values, lse the score plus log Sk
+    v = f64(x["v"])
+    u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+    mean, size = v.mean(axis=2, keepdims=True), np.abs(v).mean(axis=2, keepdims=True)
+    # the weight's rounding and the sum of Sk terms on mean |v|, the rounding of out
+    tol = (u + (Sk + 8) * 2 * 2.0 ** -24) * size + u * np.abs(mean)
+    assert (np.abs(f64(got["out"]) - mean) <= tol).all()
+    want = np.where(np.arange(Sq) % 2 == 0, -cap, cap) + np.log(Sk)
+    assert (np.abs(f64(got["lse"]) - want) <= 8 * 2.0 ** -24 * (2 * cap + 8) + (Sk + 8) * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_at_once_on_two_streams(dtype):
+    shape = (1, 4, 2, 260, 300, 64)
+    xs = [draw(*shape, dtype, seed=s) for s in (1, 2)]
+    doc = [documents(1, n, 70, seed=3) for n in (260, 300)]
+    cfg = fv.AttnConfig(softcap=30.0, doc_q=doc[0], doc_k=doc[1])
+    want = [run(x, cfg) for x in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                got.append(run(x, cfg))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(a[n], b[n]) for n in a)
+
+
 def test_long_cache_offsets_past_32_bits():
     # one key head of a cache of 2^25 + 70 tokens: byte and element offsets beyond 2^32
     S, d = (1 << 25) + 70, 128
