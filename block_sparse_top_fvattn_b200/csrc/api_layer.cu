@@ -137,7 +137,8 @@ void plan_splits(DenseArgs& a, int tile_rows_queries, int least_keys) {
   a.parts = a.splits;
 }
 // For few rows: two waves of CTAs (the second evens out sequences of unequal length), of two blocks of keys
-// at least; a cluster of a power of two up to its most, and whole clusters beyond.
+// at least; a cluster of a power of two up to its most, and whole clusters beyond. 64 key heads
+// over caches of up to 32760 keys: 139 us in 8 splits; 187 us in 5, 156 us in 16.
 void plan_few(DenseArgs& a) {
   const int64_t heads = (int64_t)a.B * a.Hkv, blocks = ((int64_t)a.Sk + kBlock - 1) / kBlock;
   const int64_t n = imax<int64_t>(1, imin((2 * kSlots + heads - 1) / heads, (blocks + 1) / 2));
