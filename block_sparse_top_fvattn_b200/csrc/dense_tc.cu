@@ -19,7 +19,9 @@
 // With rest (the output to 16 bits, for the gradients) P goes in as two bf16 terms, the second of them
 // what the rounding of the first left, behind it in the S buffer, and the second product is made twice.
 //
-// Bound by the softmax warps, whose exponentials fill the SFU, then by the products. Measured, d = 128:
+// Bound by the chain of a softmax warp's step (wait, load, maximum, exponentials, store), not by the SFU
+// alone: a polynomial on the FMA pipe for 1/8 to 1/2 of the exponentials gained nothing (packed clips 160 us
+// without, 161 to 168 with). Measured, d = 128:
 // packed clips of 16380 tokens, 6 heads: 161 us, 622 TFLOP/s; prompts of 2 x 2047 tokens, 16 / 4 heads, capped:
 // 61 us; with rest, 8192 causal tokens, 12 heads: 232 us, tensor pipe 73 % active (186 us without rest).
 //
