@@ -377,6 +377,7 @@ class LazyRouter:
         for step in range(n_steps):
             o = layer(q, k, v, step)
 
+    A step below the one before it begins a new generation: what the last one routed is dropped.
     With dense_steps > 0 the first steps, which lay out the picture, attend to all keys (dense_attn)
     and routing starts after them. from_projections takes the projections' [B, S, H, d] outputs and
     norms and rotates queries and keys first (qk_norm_rope).
@@ -393,6 +394,7 @@ class LazyRouter:
         self.csr: Optional[CsrBuffers] = None
         self.workspace: Optional[torch.Tensor] = None
         self.last_refresh: Optional[int] = None
+        self.last_step: Optional[int] = None
         self.routed = 0
 
     def should_refresh(self, step: int, shape) -> bool:
@@ -404,6 +406,9 @@ class LazyRouter:
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, step: int, *,
                  out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        if step < self.dense_steps or (self.last_step is not None and step < self.last_step):
+            self.last_refresh = None           # another generation's routing
+        self.last_step = step
         if step < self.dense_steps:
             return dense_attn(q, k, v, out=out, stream=stream)
         if self.should_refresh(step, q.shape):
