@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t s[32], packed[16];
       tc::tmem_ld32(colS, s);
       tc::tmem_ld_wait();
+      if (CAP && MASK) only32(s, see, 0.f);
       if (CAP) tanh32(s, in);
 #pragma unroll
       for (int c = 0; c < 32; c += 4) {
@@ -527,6 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!key_ok) see = 0u;
         }
       }
+      // a key behind the valid ones has no say in the cap's form; else its results alone are left out
+      if (CAP && j < a.Sk && !key_ok) see = 0u;
       const bool hidden = __any_sync(0xffffffffu, see != 0xffffffffu);
       if (ok && !warp_wait(&bars->s_full[group], turn & 1, abort)) {
         fail(&bars->abort, 10);
@@ -864,6 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_ld32(colS, s);
       tc::tmem_ld_wait();
       if (CAP) {
+        if (MASK) only32(s, see, 0.f);
         tanh32(s, map.in);
         if (BIAS) {                         // kept for the derivative: the bias takes its place
 #pragma unroll

@@ -299,15 +299,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         tc::tmem_ld32(sp, lo);
         tc::tmem_ld32(sp + 32, hi);
         tc::tmem_ld_wait();
+        const uint64_t see = visible64<DOCS>(row, doc_k, walk.doc(), j * kBlock, a.Sk, lane);
+        const bool hidden = __any_sync(0xffffffffu, see != ~0ull);
+        if (CAP && hidden) {
+          only32(lo, (uint32_t)see, 0.f);
+          only32(hi, (uint32_t)(see >> 32), 0.f);
+        }
         map.apply(lo, row.pos - j * kBlock);
         map.apply(hi, row.pos - j * kBlock - 32);
-        const uint64_t see = visible64<DOCS>(row, doc_k, walk.doc(), j * kBlock, a.Sk, lane);
-        if (__any_sync(0xffffffffu, see != ~0ull)) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (!(((uint32_t)see >> c) & 1u)) lo[c] = __float_as_uint(-INFINITY);
-            if (!(((uint32_t)(see >> 32) >> c) & 1u)) hi[c] = __float_as_uint(-INFINITY);
-          }
+        if (hidden) {
+          only32(lo, (uint32_t)see, -INFINITY);
+          only32(hi, (uint32_t)(see >> 32), -INFINITY);
         }
         if (!bounded) {
           const float mx = fmaxf(max32(lo), max32(hi)) * map.after;

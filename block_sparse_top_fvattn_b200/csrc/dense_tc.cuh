@@ -228,7 +228,15 @@ __device__ __forceinline__ void tanh32_small(uint32_t (&s)[32], float in) {
     s[c + 1] = __float_as_uint(b);
   }
 }
-// s <- tanh(s * in), by the shortest form that every score of the warp allows. The whole warp takes part.
+// x[c] stays where bit c of `see` is set and becomes `other` elsewhere.
+__device__ __forceinline__ void only32(uint32_t (&x)[32], uint32_t see, float other) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (!((see >> c) & 1u)) x[c] = __float_as_uint(other);
+}
+// s <- tanh(s * in), by the shortest form that every score of the warp allows: hidden ones have to be
+// zeros by then (only32), or what must not matter (rows that no query fills, memory behind the valid
+// keys, padding) would choose the form. The whole warp takes part.
 __device__ __forceinline__ void tanh32(uint32_t (&s)[32], float in) {
   const float top = abs_max32(s) * in;
   if (__all_sync(0xffffffffu, top <= 0.6f)) {
