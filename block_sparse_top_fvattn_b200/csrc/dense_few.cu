@@ -218,13 +218,28 @@ __global__ void __launch_bounds__(kThreads, 2)
           mma16816(sc[n], qf[2 * k + 1], f[2], f[3]);
         }
       float mx[2] = {-INFINITY, -INFINITY};
+      if (CAP) {
+        float top = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc[n][e] *= in;
+            top = fmaxf(top, fabsf(sc[n][e]));
+          }
+        // a value's form does not depend on the others', so hidden ones may be anything
+        const bool all_small = __all_sync(0xffffffffu, top <= 1.f);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) tanh_any2(sc[n][e], sc[n][e + 1], all_small, sc[n][e], sc[n][e + 1]);
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int u = e >> 1, key = first + n * 8 + c0 + (e & 1);
-          float x = CAP ? tanh_any(sc[n][e] * in) : sc[n][e];
-          x *= factor;
+          float x = sc[n][e] * factor;
           if (BIAS) x = fmaf(-row[u].slope * kLog2e, (float)abs(row[u].pos - key), x);
           const bool see = key < row[u].limit && (!DOCS || doc_k[key] == row[u].doc);
           sc[n][e] = see ? x : -INFINITY;

@@ -205,9 +205,17 @@ __device__ __forceinline__ uint64_t tanh_small2(uint64_t y) {
   for (int k = DEGREE - 1; k >= 0; --k) p = ffma2(p, u, DEGREE == 4 ? f2(c4[k % 5], c4[k % 5]) : f2(c6[k], c6[k]));
   return fmul2(p, y);
 }
-// tanh(y) = 1 - 2 / (1 + e^2y) for any y, off by a few 2^-24; e^2y at inf or 0 gives 1 and -1.
-__device__ __forceinline__ float tanh_any(float y) {
+// tanh(y) = 1 - 2 / (1 + e^2y), off by a few 2^-24; e^2y at inf or 0 gives 1 and -1. For |y| > 1 only: below,
+// the difference cancels, and times a cap of 1e6 the 2^-24 would be an error of 0.1 in a small score.
+__device__ __forceinline__ float tanh_large(float y) {
   return fmaf(-2.f, rcp(1.f + ex2(y * (2.f * kLog2e))), 1.f);
+}
+// Two values of any size, each by its own form; all_small: none of the warp's is above 1.
+__device__ __forceinline__ void tanh_any2(float y0, float y1, bool all_small, float& t0, float& t1) {
+  f2_split(tanh_small2<6>(f2(y0, y1)), t0, t1);
+  if (all_small) return;
+  if (!(fabsf(y0) <= 1.f)) t0 = tanh_large(y0);
+  if (!(fabsf(y1) <= 1.f)) t1 = tanh_large(y1);
 }
 __device__ __forceinline__ float abs_max32(const uint32_t (&s)[32]) {
   float m = 0.f;
@@ -245,7 +253,12 @@ __device__ __forceinline__ void tanh32(uint32_t (&s)[32], float in) {
     tanh32_small<6>(s, in);
   } else {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(tanh_any(__uint_as_float(s[c]) * in));
+    for (int c = 0; c < 32; c += 2) {
+      float a, b;
+      tanh_any2(__uint_as_float(s[c]) * in, __uint_as_float(s[c + 1]) * in, false, a, b);
+      s[c] = __float_as_uint(a);
+      s[c + 1] = __float_as_uint(b);
+    }
   }
 }
 
