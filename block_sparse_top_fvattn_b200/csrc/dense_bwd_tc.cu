@@ -445,8 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t s[32], packed[16];
       tc::tmem_ld32(colS, s);
       tc::tmem_ld_wait();
-      if (CAP && MASK) only32(s, see, 0.f);
-      if (CAP) tanh32(s, in);
+      if (CAP) tanh32(s, in, MASK, see);
 #pragma unroll
       for (int c = 0; c < 32; c += 4) {
         const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(&st.nlse2[col0 + c]);
@@ -867,8 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_ld32(colS, s);
       tc::tmem_ld_wait();
       if (CAP) {
-        if (MASK) only32(s, see, 0.f);
-        tanh32(s, map.in);
+        tanh32(s, map.in, MASK, see);
         if (BIAS) {                         // kept for the derivative: the bias takes its place
 #pragma unroll
           for (int c = 0; c < 32; c += 2) pw[c / 2] = f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));

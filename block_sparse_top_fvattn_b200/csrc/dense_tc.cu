@@ -301,12 +301,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         tc::tmem_ld_wait();
         const uint64_t see = visible64<DOCS>(row, doc_k, walk.doc(), j * kBlock, a.Sk, lane);
         const bool hidden = __any_sync(0xffffffffu, see != ~0ull);
-        if (CAP && hidden) {
-          only32(lo, (uint32_t)see, 0.f);
-          only32(hi, (uint32_t)(see >> 32), 0.f);
-        }
-        map.apply(lo, row.pos - j * kBlock);
-        map.apply(hi, row.pos - j * kBlock - 32);
+        map.apply(lo, row.pos - j * kBlock, hidden, (uint32_t)see);
+        map.apply(hi, row.pos - j * kBlock - 32, hidden, (uint32_t)(see >> 32));
         if (hidden) {
           only32(lo, (uint32_t)see, -INFINITY);
           only32(hi, (uint32_t)(see >> 32), -INFINITY);

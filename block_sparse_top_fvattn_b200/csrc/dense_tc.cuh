@@ -242,11 +242,20 @@ __device__ __forceinline__ void only32(uint32_t (&x)[32], uint32_t see, float ot
   for (int c = 0; c < 32; ++c)
     if (!((see >> c) & 1u)) x[c] = __float_as_uint(other);
 }
-// s <- tanh(s * in), by the shortest form that every score of the warp allows: hidden ones have to be
-// zeros by then (only32), or what must not matter (rows that no query fills, memory behind the valid
-// keys, padding) would choose the form. The whole warp takes part.
-__device__ __forceinline__ void tanh32(uint32_t (&s)[32], float in) {
-  const float top = abs_max32(s) * in;
+// s <- tanh(s * in), by the shortest form that every score of the warp allows. Hidden scores (bits of `see`
+// that are not set, where there are any) are left out, or what must not matter (rows that no query fills,
+// memory behind the valid keys, padding) would choose the form; a second look does, since most often all of
+// them are small (hiding them first took packed training with a cap from 112 to 119 us). The whole warp
+// takes part.
+__device__ __forceinline__ void tanh32(uint32_t (&s)[32], float in, bool hidden, uint32_t see) {
+  float top = abs_max32(s) * in;
+  if (hidden && !__all_sync(0xffffffffu, top <= 0.6f)) {
+    top = 0.f;
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if ((see >> c) & 1u) top = fmaxf(top, fabsf(__uint_as_float(s[c])));
+    top *= in;
+  }
   if (__all_sync(0xffffffffu, top <= 0.6f)) {
     tanh32_small<4>(s, in);
   } else if (__all_sync(0xffffffffu, top <= 1.f)) {
@@ -273,9 +282,10 @@ struct ScoreMap {
     after = BIAS ? 1.f : factor;
     slope2 = row.slope * kLog2e;
   }
-  // 32 scores in place; far = position of the row minus the first key. The whole warp takes part.
-  __device__ __forceinline__ void apply(uint32_t (&s)[32], int far) const {
-    if (CAP) tanh32(s, in);
+  // 32 scores in place; far = position of the row minus the first key; hidden, see: as for tanh32, and of
+  // hidden scores nothing is said. The whole warp takes part.
+  __device__ __forceinline__ void apply(uint32_t (&s)[32], int far, bool hidden, uint32_t see) const {
+    if (CAP) tanh32(s, in, hidden, see);
     if (BIAS) bias(s, far);
   }
   __device__ __forceinline__ void bias(uint32_t (&s)[32], int far) const {
