@@ -79,3 +79,26 @@ def test_gradients_of_small_scores_beside_large_ones(dtype):
     tol = np.einsum("bhij,bhjd->bhid", e_ds, np.abs(r["k"])) + u * np.abs(r["dq"]) + 1e-30
     far = (np.abs(f64(got["dq"]) - r["dq"]) / tol)[:, :, keep]
     assert far.max() <= 1.0, f"dq: {far.max():.2f} times its bound"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cap", [5.0, 30.0, 50.0, 51.0])
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** -100])
+@pytest.mark.parametrize("Sq", [130, 1])
+def test_values_of_any_size(dtype, cap, size, Sq):
+    # every score at the cap or at its negative: out is the mean of the values, as large or small as they are
+    Sk, d = 300, 64
+    x = draw(1, 2, 1, Sq, Sk, d, dtype)
+    sign = torch.ones(Sq, device="cuda")
+    sign[::2] = -1
+    x["q"] = (sign[:, None] * torch.ones(1, 2, Sq, d, device="cuda")).to(dtype)
+    x["k"] = torch.ones(1, 1, Sk, d, device="cuda").to(dtype)
+    x["v"] = x["v"] * size
+    got = run(x, fv.AttnConfig(softcap=cap), grads=False, scale=25.0 * cap / d)
+    v = f64(x["v"])
+    u = HALF[dtype]
+    mean, mag = v.mean(axis=2, keepdims=True), np.abs(v).mean(axis=2, keepdims=True)
+    # the weight's rounding and the sum of Sk terms on mean |v|, the rounding of out
+    tol = (u + (Sk + 8) * 2 * F) * mag + u * np.abs(mean)
+    far = np.abs(f64(got["out"]) - mean) / tol
+    assert far.max() <= 1.0, f"{far.max():.2f} times its bound"
