@@ -6,6 +6,10 @@ comes from PyTorch, every step runs in the library's kernels on one stream.
 
 Tensors may be strided as long as their last dimension is contiguous and the other strides are
 positive multiples of 16 bytes (slices of a fused projection, places in a cache, transposed views).
+
+Every call takes `stream`: it runs there instead of on the current stream, whose work it does not wait
+for. Its inputs have to be ready there, and theirs is the caller's care (record_stream) if they are freed
+before it has passed; what the call makes itself is safe on both streams.
 """
 from __future__ import annotations
 
@@ -92,8 +96,7 @@ class _Plan:
     def make(self, i: int, stream) -> torch.Tensor:
         """Output i, dense (the quickest of torch's ways to allocate a tensor)."""
         size, stride = self.outs[i]
-        t = torch.empty_strided(size, stride, dtype=self.dtype, device=self.device)
-        return t if stream is None else _made(t, stream)
+        return _made(torch.empty_strided, stream, size, stride, dtype=self.dtype, device=self.device)
 
     def run(self, *args) -> None:
         """The library's call, with the tensors' device current."""
@@ -114,10 +117,16 @@ def _handle(device: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
     return stream.cuda_stream
 
 
-def _made(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A tensor made in a call that runs on `stream`: its memory is not reused before that has passed."""
-    if stream is not None and t.numel():
-        t.record_stream(stream)
+def _made(how, stream: Optional[torch.cuda.Stream], *args, **kw) -> torch.Tensor:
+    """A tensor that a call makes. One that runs on a given stream takes it from that stream's memory: a
+    block of the current stream's could still be in use by what is queued there. The current stream, the
+    caller's, may use it too, so its memory is not given away before that has passed."""
+    if stream is None:
+        return how(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = how(*args, **kw)
+    if t.numel():
+        t.record_stream(torch.cuda.current_stream(kw["device"]))
     return t
 
 
@@ -130,7 +139,7 @@ def _scratch(plan: _Plan, given: Optional[torch.Tensor], stream) -> Optional[tor
         return given
     if plan.nws == 0:
         return None
-    return _made(torch.empty(plan.nws, dtype=torch.uint8, device=plan.device), stream)
+    return _made(torch.empty, stream, plan.nws, dtype=torch.uint8, device=plan.device)
 
 
 # ------------------------------------------------------------------ norm and rotation
@@ -252,8 +261,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
         dk = plan.make(1, stream)
     dwq = dwk = None
     if q_weight is not None:
-        dwq = _made(torch.empty(q.shape[3], dtype=torch.float32, device=plan.device), stream)
-        dwk = _made(torch.empty(q.shape[3], dtype=torch.float32, device=plan.device), stream)
+        dwq = _made(torch.empty, stream, q.shape[3], dtype=torch.float32, device=plan.device)
+        dwk = _made(torch.empty, stream, q.shape[3], dtype=torch.float32, device=plan.device)
     ws = _scratch(plan, workspace, stream)
     plan.run(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), plan.ref, _ptr(q_weight), _ptr(k_weight),
              _ptr(cos), _ptr(sin), _ptr(positions), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws),
