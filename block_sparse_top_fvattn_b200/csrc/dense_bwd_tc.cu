@@ -386,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
+    __syncwarp();
+    if (share > 1) named_sync(3, kThreads);      // see the results
   } else {
     // ------------------------------------------------------------ elementwise
     tc::regs_up<kRegsWork>();
@@ -562,6 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(&bars->drain, 0, abort)) fail(&bars->abort, 12);
       tc::fence_after_sync();
     }
+    // A cluster's results go over the tiles. After an abort copies and products may still be on their way to or
+    // from them: the other warps come here once theirs have ended.
+    if (share > 1) named_sync(3, kThreads);
     const bool broken = __any_sync(0xffffffffu, *abort != 0);
     const int part_d = (warp >> 2) & 1;
     const float by = broken ? __int_as_float(0x7fffffff) : group == 0 ? 1.f : a.scale;
@@ -585,7 +590,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (share == 1) {
         if (j < a.Sk) store32(dst + cc * 32, o, by);
       } else {
-        // over the tiles: every product of the CTA is done
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
           *reinterpret_cast<float4*>(shared_row + cc * 32 + e) =
