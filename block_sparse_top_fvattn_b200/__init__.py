@@ -22,7 +22,8 @@ import torch
 from . import _lib
 from ._lib import (FVATTN_BF16, FVATTN_F32, FVATTN_MODE_FRAME_TOPK, FVATTN_MODE_TOPP, FvattnError, check,
                    load, status_string)
-from .around import AttnConfig, dense_attn, dense_attn_bwd, qk_norm_rope, qk_norm_rope_bwd
+from .around import (AttnConfig, dense_attn, dense_attn_bwd, dense_attn_bwd_timeout_check,
+                     dense_attn_timeout_check, qk_norm_rope, qk_norm_rope_bwd)
 
 __all__ = ["RouteConfig", "CsrBuffers", "alloc_csr", "route", "route_pool", "route_finish", "sparse_attn",
            "sparse_attn_stamped",
@@ -30,7 +31,8 @@ __all__ = ["RouteConfig", "CsrBuffers", "alloc_csr", "route", "route_pool", "rou
            "block_scores_timeout_check",
            "read_status",
            "workspace_bytes", "shape_of", "load", "FvattnError", "status_string", "rlb_plan", "select_heads",
-           "LazyRouter", "qk_norm_rope", "qk_norm_rope_bwd", "AttnConfig", "dense_attn", "dense_attn_bwd"]
+           "LazyRouter", "qk_norm_rope", "qk_norm_rope_bwd", "AttnConfig", "dense_attn", "dense_attn_bwd",
+           "dense_attn_timeout_check", "dense_attn_bwd_timeout_check"]
 
 BLOCK = 64
 

@@ -169,6 +169,12 @@ def load() -> ctypes.CDLL:
     lib.fvattn_dense_attn_bwd.restype = ctypes.c_int
     lib.fvattn_dense_attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, P(DenseShape), P(DenseMask), vp, vp, vp, vp,
                                           ctypes.c_size_t, vp, vp]
+    lib.fvattn_dense_attn_timeout_check.restype = ctypes.c_int
+    lib.fvattn_dense_attn_timeout_check.argtypes = [vp, vp, vp, P(DenseShape), P(DenseMask), vp, vp, vp, vp,
+                                                    ctypes.c_size_t, vp, ctypes.c_uint32, ctypes.c_uint32, vp]
+    lib.fvattn_dense_attn_bwd_timeout_check.restype = ctypes.c_int
+    lib.fvattn_dense_attn_bwd_timeout_check.argtypes = [vp, vp, vp, vp, vp, vp, vp, P(DenseShape), P(DenseMask), vp, vp, vp,
+                                                        vp, ctypes.c_size_t, vp, ctypes.c_uint32, ctypes.c_uint32, vp]
     _lib = lib
     return lib
 

@@ -20,9 +20,10 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from ._lib import FVATTN_BF16, FVATTN_F32, FVATTN_OK, FvattnError, load
+from ._lib import FVATTN_BF16, FVATTN_F32, FVATTN_OK, FvattnError, check, load
 
-__all__ = ["qk_norm_rope", "qk_norm_rope_bwd", "AttnConfig", "dense_attn", "dense_attn_bwd"]
+__all__ = ["qk_norm_rope", "qk_norm_rope_bwd", "AttnConfig", "dense_attn", "dense_attn_bwd",
+           "dense_attn_timeout_check", "dense_attn_bwd_timeout_check"]
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -416,3 +417,41 @@ def dense_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
              plan.ref, ctypes.byref(cfg.to_c()), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), plan.nws,
              _ptr(status), handle)
     return dq, dk, dv
+
+
+def dense_attn_timeout_check(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cfg: Optional[AttnConfig] = None, *,
+                             step: int = 0, polls: int = 64, scale: float = 0.0):
+    """fvattn_dense_attn_timeout_check: dense_attn (bf16) whose waits run out on purpose at each CTA's step
+    `step`. Returns (the device status word afterwards, its detail, out, lse): FVATTN_ERR_TIMEOUT and NaN
+    rows where a CTA had that many steps."""
+    cfg = cfg or AttnConfig()
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    status = torch.zeros(4, dtype=torch.int32, device=q.device)
+    plan = _dense_plan(q, k, v, cfg, scale, None, None, lse, status, None)
+    out, ws = plan.make(0, None), _scratch(plan, None, None)
+    with torch.cuda.device(plan.device):
+        check(load().fvattn_dense_attn_timeout_check(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), plan.ref, ctypes.byref(cfg.to_c()), out.data_ptr(), None,
+            lse.data_ptr(), _ptr(ws), plan.nws, status.data_ptr(), int(step), int(polls), _handle(plan.device, None)),
+            "fvattn_dense_attn_timeout_check")
+    code, detail = status[:2].tolist()
+    return code, detail, out, lse
+
+
+def dense_attn_bwd_timeout_check(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                                 lse: torch.Tensor, cfg: Optional[AttnConfig] = None, *, step: int = 0, polls: int = 64,
+                                 scale: float = 0.0):
+    """fvattn_dense_attn_bwd_timeout_check: the same of dense_attn_bwd. Returns (status word, detail, dq, dk,
+    dv)."""
+    cfg = cfg or AttnConfig()
+    status = torch.zeros(4, dtype=torch.int32, device=q.device)
+    plan = _dense_plan(q, k, v, cfg, scale, out, None, lse, status, (dout, None, None, None))
+    dq, dk, dv = (plan.make(i, None) for i in range(3))
+    ws = _scratch(plan, None, None)
+    with torch.cuda.device(plan.device):
+        check(load().fvattn_dense_attn_bwd_timeout_check(
+            dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None, lse.data_ptr(), plan.ref,
+            ctypes.byref(cfg.to_c()), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), plan.nws, status.data_ptr(),
+            int(step), int(polls), _handle(plan.device, None)), "fvattn_dense_attn_bwd_timeout_check")
+    code, detail = status[:2].tolist()
+    return code, detail, dq, dk, dv

@@ -10,7 +10,7 @@ using namespace fv;
 
 namespace {
 
-constexpr int kVersion = (1 << 16) | 4;
+constexpr int kVersion = (1 << 16) | 5;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

@@ -202,6 +202,91 @@ DenseArgs fwd_args(const fvattn_dense_shape* s, const fvattn_dense_mask* m) {
   return a;
 }
 
+int dense_attn(const void* q, const void* k, const void* v, const fvattn_dense_shape* shape,
+               const fvattn_dense_mask* mask, void* out, void* rest, float* lse, void* workspace, size_t workspace_bytes,
+               int32_t* status, fvattn_stream_t stream, uint32_t hold_polls = 0, uint32_t hold_step = 0) {
+  const int st = validate_dense(shape, mask, false);
+  if (st != FVATTN_OK) return st;
+  if (!q || !k || !v || !out) return FVATTN_ERR_INVALID;
+  for (const void* p : {q, k, v, (const void*)out, (const void*)rest})
+    if (!aligned(p, 16)) return FVATTN_ERR_INVALID;
+  if (!aligned(lse, 4) || !aligned(status, 4)) return FVATTN_ERR_INVALID;
+  if (rest != nullptr && shape->dtype != FVATTN_BF16) return FVATTN_ERR_INVALID;
+  DenseArgs a = fwd_args(shape, mask);
+  const DenseWs w = fwd_ws(a, shape->dtype);
+  if (w.total > 0 && (workspace == nullptr || !aligned(workspace, 256))) return FVATTN_ERR_INVALID;
+  if (workspace_bytes < w.total) return FVATTN_ERR_CAPACITY;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.rest = rest;
+  a.lse = lse;
+  a.status = status;
+  a.hold_polls = hold_polls;
+  a.hold_step = hold_step;
+  if (a.parts > 1) {
+    a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
+    a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
+    a.doc_size_k = kBlock;
+    e = launch_dense_prepare(a, shape->dtype, s);
+  }
+  if (e == cudaSuccess)
+    e = shape->dtype == FVATTN_F32 ? launch_dense_f32(a, s)
+        : few_rows(a, shape->dtype) ? launch_dense_few(a, s)
+                                    : launch_dense_tc(a, s);
+  if (e == cudaSuccess && a.parts > 1) e = launch_dense_combine(a, shape->dtype, s);
+  return cuda_status(e);
+}
+
+int dense_attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out, const void* rest,
+                   const float* lse, const fvattn_dense_shape* shape, const fvattn_dense_mask* mask, void* dq, void* dk,
+                   void* dv, void* workspace, size_t workspace_bytes, int32_t* status, fvattn_stream_t stream,
+                   uint32_t hold_polls = 0, uint32_t hold_step = 0) {
+  const int st = validate_dense(shape, mask, true);
+  if (st != FVATTN_OK) return st;
+  if (!dout || !q || !k || !v || !out || !lse || !dq || !dk || !dv) return FVATTN_ERR_INVALID;
+  for (const void* p : {dout, q, k, v, out, rest, (const void*)dq, (const void*)dk, (const void*)dv})
+    if (!aligned(p, 16)) return FVATTN_ERR_INVALID;
+  if (!aligned(lse, 4) || !aligned(status, 4)) return FVATTN_ERR_INVALID;
+  if (rest != nullptr && shape->dtype != FVATTN_BF16) return FVATTN_ERR_INVALID;
+  DenseArgs a = dense_args(shape, mask);
+  const DenseWs w = bwd_ws(a, shape->dtype);
+  if (workspace == nullptr || !aligned(workspace, 256)) return FVATTN_ERR_INVALID;
+  if (workspace_bytes < w.total) return FVATTN_ERR_CAPACITY;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = const_cast<void*>(out);
+  a.rest = const_cast<void*>(rest);
+  a.lse = const_cast<float*>(lse);
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.delta = reinterpret_cast<float*>(ws + w.delta);
+  a.status = status;
+  a.hold_polls = hold_polls;
+  a.hold_step = hold_step;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
+    a.doc_blocks_q = reinterpret_cast<int2*>(ws + w.docs_q);
+    a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
+    a.doc_size_q = kBwdRows / a.G;
+    a.doc_size_k = kBwdKeys;
+  }
+  cudaError_t e = launch_dense_prepare(a, shape->dtype, s);
+  if (e == cudaSuccess) e = shape->dtype == FVATTN_BF16 ? launch_dense_bwd_tc(a, s) : launch_dense_f32_bwd(a, s);
+  return cuda_status(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -277,42 +362,16 @@ size_t fvattn_dense_attn_workspace_bytes(const fvattn_dense_shape* shape, const 
 int fvattn_dense_attn(const void* q, const void* k, const void* v, const fvattn_dense_shape* shape,
                       const fvattn_dense_mask* mask, void* out, void* rest, float* lse, void* workspace,
                       size_t workspace_bytes, int32_t* status, fvattn_stream_t stream) {
-  const int st = validate_dense(shape, mask, false);
-  if (st != FVATTN_OK) return st;
-  if (!q || !k || !v || !out) return FVATTN_ERR_INVALID;
-  for (const void* p : {q, k, v, (const void*)out, (const void*)rest})
-    if (!aligned(p, 16)) return FVATTN_ERR_INVALID;
-  if (!aligned(lse, 4) || !aligned(status, 4)) return FVATTN_ERR_INVALID;
-  if (rest != nullptr && shape->dtype != FVATTN_BF16) return FVATTN_ERR_INVALID;
-  DenseArgs a = fwd_args(shape, mask);
-  const DenseWs w = fwd_ws(a, shape->dtype);
-  if (w.total > 0 && (workspace == nullptr || !aligned(workspace, 256))) return FVATTN_ERR_INVALID;
-  if (workspace_bytes < w.total) return FVATTN_ERR_CAPACITY;
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.out = out;
-  a.rest = rest;
-  a.lse = lse;
-  a.status = status;
-  if (a.parts > 1) {
-    a.part_o = reinterpret_cast<float*>(ws + w.part_o);
-    a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-  }
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
-    a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
-    a.doc_size_k = kBlock;
-    e = launch_dense_prepare(a, shape->dtype, s);
-  }
-  if (e == cudaSuccess)
-    e = shape->dtype == FVATTN_F32 ? launch_dense_f32(a, s)
-        : few_rows(a, shape->dtype) ? launch_dense_few(a, s)
-                                    : launch_dense_tc(a, s);
-  if (e == cudaSuccess && a.parts > 1) e = launch_dense_combine(a, shape->dtype, s);
-  return cuda_status(e);
+  return dense_attn(q, k, v, shape, mask, out, rest, lse, workspace, workspace_bytes, status, stream);
+}
+
+int fvattn_dense_attn_timeout_check(const void* q, const void* k, const void* v, const fvattn_dense_shape* shape,
+                                    const fvattn_dense_mask* mask, void* out, void* rest, float* lse, void* workspace,
+                                    size_t workspace_bytes, int32_t* status, uint32_t step, uint32_t polls,
+                                    fvattn_stream_t stream) {
+  if (polls == 0 || status == nullptr) return FVATTN_ERR_INVALID;
+  if (shape != nullptr && shape->dtype == FVATTN_F32) return FVATTN_ERR_UNSUPPORTED;
+  return dense_attn(q, k, v, shape, mask, out, rest, lse, workspace, workspace_bytes, status, stream, polls, step);
 }
 
 size_t fvattn_dense_attn_bwd_workspace_bytes(const fvattn_dense_shape* shape, const fvattn_dense_mask* mask) {
@@ -324,40 +383,19 @@ int fvattn_dense_attn_bwd(const void* dout, const void* q, const void* k, const 
                           const void* rest, const float* lse, const fvattn_dense_shape* shape,
                           const fvattn_dense_mask* mask, void* dq, void* dk, void* dv, void* workspace,
                           size_t workspace_bytes, int32_t* status, fvattn_stream_t stream) {
-  const int st = validate_dense(shape, mask, true);
-  if (st != FVATTN_OK) return st;
-  if (!dout || !q || !k || !v || !out || !lse || !dq || !dk || !dv) return FVATTN_ERR_INVALID;
-  for (const void* p : {dout, q, k, v, out, rest, (const void*)dq, (const void*)dk, (const void*)dv})
-    if (!aligned(p, 16)) return FVATTN_ERR_INVALID;
-  if (!aligned(lse, 4) || !aligned(status, 4)) return FVATTN_ERR_INVALID;
-  if (rest != nullptr && shape->dtype != FVATTN_BF16) return FVATTN_ERR_INVALID;
-  DenseArgs a = dense_args(shape, mask);
-  const DenseWs w = bwd_ws(a, shape->dtype);
-  if (workspace == nullptr || !aligned(workspace, 256)) return FVATTN_ERR_INVALID;
-  if (workspace_bytes < w.total) return FVATTN_ERR_CAPACITY;
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.out = const_cast<void*>(out);
-  a.rest = const_cast<void*>(rest);
-  a.lse = const_cast<float*>(lse);
-  a.dout = dout;
-  a.dq = dq;
-  a.dk = dk;
-  a.dv = dv;
-  a.delta = reinterpret_cast<float*>(ws + w.delta);
-  a.status = status;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (shape->dtype == FVATTN_BF16 && a.mask.doc_k != nullptr) {
-    a.doc_blocks_q = reinterpret_cast<int2*>(ws + w.docs_q);
-    a.doc_blocks_k = reinterpret_cast<int2*>(ws + w.docs_k);
-    a.doc_size_q = kBwdRows / a.G;
-    a.doc_size_k = kBwdKeys;
-  }
-  cudaError_t e = launch_dense_prepare(a, shape->dtype, s);
-  if (e == cudaSuccess) e = shape->dtype == FVATTN_BF16 ? launch_dense_bwd_tc(a, s) : launch_dense_f32_bwd(a, s);
-  return cuda_status(e);
+  return dense_attn_bwd(dout, q, k, v, out, rest, lse, shape, mask, dq, dk, dv, workspace, workspace_bytes, status,
+                        stream);
+}
+
+int fvattn_dense_attn_bwd_timeout_check(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                                        const void* rest, const float* lse, const fvattn_dense_shape* shape,
+                                        const fvattn_dense_mask* mask, void* dq, void* dk, void* dv, void* workspace,
+                                        size_t workspace_bytes, int32_t* status, uint32_t step, uint32_t polls,
+                                        fvattn_stream_t stream) {
+  if (polls == 0 || status == nullptr) return FVATTN_ERR_INVALID;
+  if (shape != nullptr && shape->dtype == FVATTN_F32) return FVATTN_ERR_UNSUPPORTED;
+  return dense_attn_bwd(dout, q, k, v, out, rest, lse, shape, mask, dq, dk, dv, workspace, workspace_bytes, status,
+                        stream, polls, step);
 }
 
 }  // extern "C"

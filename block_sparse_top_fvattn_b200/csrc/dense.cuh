@@ -35,6 +35,7 @@ struct DenseArgs {
   int2 *doc_blocks_q, *doc_blocks_k;
   int doc_size_q, doc_size_k;
   int32_t* status;
+  uint32_t hold_polls, hold_step; // failure-path check: each loader's wait at this step runs out; 0: none
 };
 
 constexpr int kPosMax = (1 << 30) - 1;

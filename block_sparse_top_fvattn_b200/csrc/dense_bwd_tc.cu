@@ -139,6 +139,7 @@ struct DkvBars {
   uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2];      // by parity of the step
   uint64_t dv_done[2], dk_done[2];
   uint64_t drain;
+  uint64_t hold;                      // never completes (failure-path check)
   int doc_lo, doc_hi, doc_pad;        // documents of the keys
   uint32_t tmem_base;
   int abort;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars->ds_full[s], kWork / 2);
     }
     tc::mbar_init(&bars->drain, 3);
+    tc::mbar_init(&bars->hold, 1);
     bars->abort = 0;
     bars->doc_lo = 0x7fffffff;
     bars->doc_hi = -1;
@@ -280,6 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool ok = true;
       for (int t; ok && (t = walk.next(lane, share)) >= 0; ++g) {
+        if (held(a, &bars->hold, abort, g)) {
+          fail(&bars->abort, 20);
+          ok = false;
+          break;
+        }
         const uint32_t sq = g % kStagesQ, sg = g % kStagesG;
         const bool pad = DOCS && walk.doc().x < 0;
         ok = load(tmQ, a.q, a.qs, &bars->q_full[sq], &bars->q_empty[sq], ((g / kStagesQ) & 1) ^ 1,
@@ -648,6 +655,7 @@ struct DqBars {
   uint64_t s_full[2], dq_done[2];      // by parity of the step
   uint64_t dp_full, ds_full;
   uint64_t drain;
+  uint64_t hold;                       // never completes (failure-path check)
   int doc_lo, doc_hi;
   uint32_t tmem_base;
   int abort;
@@ -694,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&bars->dp_full, 1);
     tc::mbar_init(&bars->ds_full, kWork);
     tc::mbar_init(&bars->drain, 2);
+    tc::mbar_init(&bars->hold, 1);
     bars->abort = 0;
     bars->doc_lo = 0x7fffffff;
     bars->doc_hi = -1;
@@ -729,6 +738,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0, k_armed = 0, v_armed = 0;      // steps whose copies were issued
       bool q_armed = false, ok = true;
       for (int j; ok && (j = walk.next(lane)) >= 0; ++g) {
+        if (held(a, &bars->hold, abort, g)) {
+          fail(&bars->abort, 20);
+          ok = false;
+          break;
+        }
         const uint32_t sk = g % 3, sv = g & 1;
         unsigned char* dk = smem + L::kOffK + sk * L::kTile;
         if (g == 0) {

@@ -37,6 +37,7 @@ constexpr int kRows = 16;
 
 struct FewBars {
   uint64_t full[kStages], empty[kStages];
+  uint64_t hold;                               // never completes (failure-path check)
   float m[kWork][kRows], l[kWork][kRows];      // statistics of the warps
   int doc_lo, doc_hi;
   int abort;
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc::mbar_init(&bars->full[s], 1);
       tc::mbar_init(&bars->empty[s], kWork);
     }
+    tc::mbar_init(&bars->hold, 1);
     bars->abort = 0;
     int lo = 0x7fffffff, hi = -1;
     if (DOCS) {
@@ -144,6 +146,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t g = 0, armed = 0;
     for (int j; (j = walk.next(lane)) >= 0; ++g) {
       const int s = g % kStages;
+      if (held(a, &bars->hold, abort, g)) {
+        fail(&bars->abort, 20);
+        break;
+      }
       if (!warp_wait(&bars->empty[s], ((g / kStages) & 1) ^ 1, abort)) {
         fail(&bars->abort, 1);
         break;

@@ -69,6 +69,7 @@ struct FwdBars {
   uint64_t p_full[2];     // P written by the four softmax warps and V landed (the V loader's arrival)
   uint64_t pv_done[2];    // P V done: O is stable, the V stage may be refilled
   uint64_t drain;         // every product of the CTA is done
+  uint64_t hold;          // never completes (failure-path check)
   int p_arrived[4];       // per softmax warp: the last step whose P it published
   int v_armed;            // the last step whose V copy was issued
   int doc_lo, doc_hi;     // documents of the tile's rows
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       tc::mbar_init(&bars->pv_done[s], 1);
     }
     tc::mbar_init(&bars->drain, 1);
+    tc::mbar_init(&bars->hold, 1);
     for (int w = 0; w < 4; ++w) bars->p_arrived[w] = -1;
     bars->v_armed = -1;
     bars->abort = 0;
@@ -189,6 +191,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     bool padded = false;         // block `before` has padding keys
     bool ok = true;
     for (int j; ok && (j = walk.next(lane)) >= 0; ++g) {
+      if (held(a, &bars->hold, abort, g)) {
+        fail(&bars->abort, 20);
+        ok = false;
+        break;
+      }
       if (g == 0 && lane == 0) {
         tc::mbar_expect_tx(&bars->q_full, (uint32_t)(qpt * a.G) * 128 * (D / 64));
         q_armed = true;

@@ -24,6 +24,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xffffffffu, ok);
 }
 
+// The failure-path check's wait, at step g of a loader: on a barrier that nothing completes. A whole warp.
+__device__ __forceinline__ bool held(const DenseArgs& a, uint64_t* hold, const volatile int* abort, uint32_t g) {
+  if (a.hold_polls == 0 || g != a.hold_step) return false;
+  return !__all_sync(0xffffffffu, tc::mbar_wait(hold, 0, abort, a.hold_polls));
+}
+
 // A barrier among `threads` threads of the CTA (id 0 is __syncthreads').
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");

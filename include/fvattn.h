@@ -486,6 +486,26 @@ int fvattn_dense_attn_bwd(const void* dout, const void* q, const void* k, const 
                           void* dk, void* dv, void* workspace, size_t workspace_bytes,
                           int32_t* status, fvattn_stream_t stream);
 
+/*
+ * Failure-path checks of the bounded waits of the bf16 kernels (as fvattn_sparse_attn_timeout_check):
+ * the loader of every CTA waits at its step `step` (from 0; one step is one block of keys, or one group
+ * of rows in dK and dV) on a barrier that nothing completes, for `polls` (>= 1) polls. Every CTA with
+ * more steps than that stops with copies and products of the steps before in flight, waits for those,
+ * frees its tensor memory, writes NaN rows and leaves FVATTN_ERR_TIMEOUT in status[0], which must not be
+ * NULL here; the stream stays usable. Other CTAs run as always. FVATTN_ERR_UNSUPPORTED for fp32, whose
+ * kernels have no such waits.
+ */
+int fvattn_dense_attn_timeout_check(const void* q, const void* k, const void* v, const fvattn_dense_shape* shape,
+                                    const fvattn_dense_mask* mask, void* out, void* rest, float* lse,
+                                    void* workspace, size_t workspace_bytes, int32_t* status, uint32_t step,
+                                    uint32_t polls, fvattn_stream_t stream);
+int fvattn_dense_attn_bwd_timeout_check(const void* dout, const void* q, const void* k, const void* v,
+                                        const void* out, const void* rest, const float* lse,
+                                        const fvattn_dense_shape* shape, const fvattn_dense_mask* mask,
+                                        void* dq, void* dk, void* dv, void* workspace,
+                                        size_t workspace_bytes, int32_t* status, uint32_t step,
+                                        uint32_t polls, fvattn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
