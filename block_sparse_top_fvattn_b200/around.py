@@ -60,6 +60,12 @@ def _strides(t: torch.Tensor, tokens_first: bool = False) -> _lib.Strides:
     return _lib.Strides(b, y, x) if tokens_first else _lib.Strides(b, x, y)
 
 
+def _need(**tensors) -> None:
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} must be given")
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -193,6 +199,8 @@ def _qk_plan(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps, ou
     plan = _plans.get(key)
     if plan is not None:
         return plan
+    if grads is not None:
+        _need(dq_out=outs[0], dk_out=outs[1])
     shp = _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps)
     if status is not None:
         _check(status, "status", (4,), q, torch.int32)
@@ -340,6 +348,8 @@ def _dense_plan(q, k, v, cfg: AttnConfig, scale, out, rest, lse, status, grads) 
     plan = _plans.get(key)
     if plan is not None:
         return plan
+    if grads is not None:
+        _need(dout=grads[0], out=out, lse=lse)
     shp = _dense_shape(q, k, v, cfg, scale)
     cfg.check(q, k.shape[2])
     if status is not None:
