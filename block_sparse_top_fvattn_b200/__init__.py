@@ -115,6 +115,12 @@ def _check_tensor(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be contiguous [B, H, S, d]")
 
 
+def _check_out(out: torch.Tensor, q: torch.Tensor) -> None:
+    """The kernels write q's elements in q's order from out's first address on."""
+    if not out.is_contiguous() or out.numel() != q.numel() or out.dtype != q.dtype or out.device != q.device:
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor of {q.numel()} elements on {q.device}")
+
+
 def alloc_csr(B: int, H: int, S: int, device="cuda", codes: bool = False) -> CsrBuffers:
     """Router output buffers; `codes` adds the per-entry token masks that token-exact frame
     mode (RouteConfig.frame_exact) writes and the attention applies."""
@@ -213,6 +219,8 @@ def sparse_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, csr: CsrBuffe
             raise ValueError("q, k, v must have the same shape and dtype")
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _check_out(out, q)
     shp = shape_of(q, scale)
     c_csr = csr.to_c()
     check(load().fvattn_sparse_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(shp), ctypes.byref(c_csr),
@@ -232,6 +240,8 @@ def sparse_attn_stamped(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, csr: 
             raise ValueError("q, k, v must have the same shape and dtype")
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _check_out(out, q)
     shp = shape_of(q, scale)
     lib = load()
     words = lib.fvattn_attn_stamp_words(ctypes.byref(shp))
@@ -431,7 +441,8 @@ class LazyRouter:
                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """The layer on the projections q, k, v [B, S, H, d] (any strides with a contiguous last
         dimension): norm and rotation of q and k (qk_norm_rope's arguments), then this step's attention.
-        Returns [B, H, S, d]."""
+        Returns [B, H, S, d]; out, when given, has to be contiguous on routed steps, which also need as many
+        key heads as query heads."""
         q, k = qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=positions, interleaved=interleaved, eps=eps)
         v = v.transpose(1, 2)
         return self(q, k, v if step < self.dense_steps else v.contiguous(), step, out=out)
