@@ -367,7 +367,9 @@ def _dense_plan(q, k, v, cfg: AttnConfig, scale, out, rest, lse, status, grads) 
     shp.o = strides(out, "out", q)
     if rest is not None:
         r = strides(rest, "rest", q)
-        if q.dtype != torch.bfloat16 or (r.b, r.h, r.s) != (shp.o.b, shp.o.h, shp.o.s):
+        o = shp.o
+        if q.dtype != torch.bfloat16 or any(n > 1 and x != y for n, x, y in
+                                            zip(q.shape, (r.b, r.h, r.s), (o.b, o.h, o.s))):
             raise ValueError("rest must be bf16 and have out's strides")
     lib = load()
     name = "fvattn_dense_attn" if grads is None else "fvattn_dense_attn_bwd"
