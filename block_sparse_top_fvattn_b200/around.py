@@ -290,7 +290,8 @@ class AttnConfig:
     slopes      fp32 [Hq]: the score falls by slope * |p - j| (after the cap)
     q_start     int32 [B]: position of each sequence's first query; None: Sk - Sq
     prefix_len  int32 [B], with causal: keys below it are visible to every query
-    kv_len      int32 [B]: keys from kv_len on do not exist, whatever their memory holds
+    kv_len      int32 [B]: keys from kv_len on do not exist, whatever their memory holds (nor, with causal, do
+                those behind every query and prefix; other hidden keys have to hold numbers)
     doc_q, doc_k  int32 [B, Sq] and [B, Sk]: a query sees only keys of its document number; a negative
                 number is padding, which sees nothing and is seen by nothing, whatever it holds
     """

@@ -43,7 +43,7 @@ constexpr int kPosMax = (1 << 30) - 1;
 // What masks one sequence of the batch.
 struct DenseSeq {
   int q0;        // position of the first query
-  int kv;        // keys that exist
+  int kv;        // keys that exist (those that some query may see)
   int prefix;    // keys visible to every query (causal)
 };
 
@@ -52,6 +52,8 @@ __device__ __forceinline__ DenseSeq dense_seq(const DenseArgs& a, int b) {
   s.q0 = a.mask.q_start != nullptr ? min(max(a.mask.q_start[b], -kPosMax), kPosMax) : a.Sk - a.Sq;
   s.kv = a.mask.kv_len != nullptr ? min(max(a.mask.kv_len[b], 0), a.Sk) : a.Sk;
   s.prefix = a.mask.prefix_len != nullptr ? a.mask.prefix_len[b] : 0;
+  // under an order nobody sees what is behind the last query (of a cache that is longer): as if it did not exist
+  if (a.causal) s.kv = max(0, min(s.kv, max(s.q0 + a.Sq, s.prefix)));
   return s;
 }
 

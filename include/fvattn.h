@@ -441,9 +441,12 @@ typedef struct {
  * What biases and masks the scores; every pointer is a device array or NULL.
  *  slopes      float [Hq]: the score of (query position p, key j) falls by slope * |p - j| (after
  *              the cap).
- *  q_start     int32 [B]: position of a sequence's first query; NULL: Sk - Sq.
+ *  q_start     int32 [B]: position of a sequence's first query, clamped to +-(2^30 - 1); NULL: Sk - Sq.
  *  kv_len      int32 [B]: keys from kv_len on do not exist (their K and V are never used, whatever
  *              they hold); values outside [0, Sk] are clamped. NULL: Sk.
+ *              Nor, with causal, do keys that are behind every query and prefix of their sequence. Other
+ *              hidden keys have to hold numbers: a NaN or an infinity among the keys that some query sees may
+ *              make NaN of rows that do not see it.
  *  prefix_len  int32 [B]: with causal, keys below it are visible to every query.
  *  doc_q, doc_k int32 [B, Sq] and [B, Sk], both or neither: a query sees only keys of an equal
  *              document number; a negative number is padding, sees nothing and is seen by nothing
