@@ -10,6 +10,9 @@ positive multiples of 16 bytes (slices of a fused projection, places in a cache,
 Every call takes `stream`: it runs there instead of on the current stream, whose work it does not wait
 for. Its inputs have to be ready there, and theirs is the caller's care (record_stream) if they are freed
 before it has passed; what the call makes itself is safe on both streams.
+
+Nothing here records itself for autograd: outputs never require gradients. A training step calls the _bwd
+functions itself, or from a torch.autograd.Function of its own.
 """
 from __future__ import annotations
 

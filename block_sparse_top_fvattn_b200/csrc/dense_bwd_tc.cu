@@ -18,8 +18,9 @@
 // dQ: lane = row; S has two buffers, so S(i+1) is ready when dS(i) is done:
 //   products   dP(i+1) dQ(i) S(i+2);   warps   P(i+1), then dS(i+1) from dP(i+1)
 //
-// P and dS are rounded to bf16 as the products' operands; lse, delta and all sums stay in fp32, and
-// the scale is applied once to the sums.
+// P and dS are rounded to bf16 as the products' operands: the results are off by 0.0024 of their size, where an
+// fp32 computation rounded once is off by 0.0017, and a second term of each would double these products. lse,
+// delta and all sums stay in fp32, and the scale is applied once to the sums.
 //
 // Bound by the chain from products to elementwise work and back. Measured at 8192 tokens, causal, 12 heads,
 // d = 128: dK/dV 366 us (tensor pipe 56 % active), dQ 255 us (62 %, SFU 42 %), in a loop at the board's power
@@ -54,7 +55,7 @@ constexpr int kLoader = 16, kMmaS = 17, kMmaOut = 18, kMmaDp = 19;
 // Registers: of the 96 per thread at the launch the last four warps give up 56, the sixteen take 8 more
 // (128 x 40 + 512 x 104 = 58,368 of the launch's 61,440). With the document code under a template argument: 387
 // to 366 us; with 182 bytes of spill stores it had taken 547 us. Left in dK/dV: none to 8 bytes plain and capped,
-// 20 to 32 with a bias, 32 to 98 with documents.
+// 20 with a bias, 70 with a bias and a cap, 44 to 114 with documents.
 constexpr int kRegsWork = 104, kRegsOther = 40;
 constexpr int kWork = 16;
 constexpr int kCols = kT * 4 / kWork; // columns of a score tile per thread

@@ -10,7 +10,8 @@
 // A CTA takes 64 rows (forward, dQ) or 64 keys (dK, dV) and walks over the other side in tiles of
 // 64, operands in shared memory as fp32, a 4 x 4 piece of the 64 x 64 scores and a 4 x d/16 piece
 // of each result per thread in registers. Bound by the fp32 pipe and the shared-memory loads that
-// feed it. Every sum has a fixed order. Measured: 1024 tokens, 2 heads of 64, capped: 31 us, 9 TFLOP/s.
+// feed it. Every sum has a fixed order. Tiles are skipped by limit, not by document. Measured: 1024 tokens, 2
+// heads of 64, capped: 31.6 us, 9 TFLOP/s; 2000 tokens, 8 / 2 heads: 313 us, gradients 2098 us.
 #include <cuda_bf16.h>
 
 #include "dense.cuh"

@@ -11,8 +11,12 @@
 // eight, which join their results through distributed shared memory; only where eight are not enough
 // do partial results go through memory and a second kernel.
 //
+// P is rounded to bf16 for the second product, and goes in as two bf16 terms with rest: without it outputs are
+// off by 0.0018 of their size, where an fp32 computation rounded once is off by 0.0017; the second term always
+// would cost 2 us of the 136.
+//
 // Measured: single tokens over 8 caches of up to 32760, 32 / 8 heads, capped: 136 us, 95 % of the copy rate
-// (tiles of 128 rows on tcgen05: 193 us); 4 caches of up to 1000, 8 / 2 heads: 7.5 us (15 us).
+// (tiles of 128 rows on tcgen05: 193 us); 4 caches of up to 1000, 8 / 2 heads: 6.7 us (15 us).
 //
 // Every wait is bounded; one that runs out is reported in the status word and makes the rows NaN.
 #include <cooperative_groups.h>

@@ -9,7 +9,7 @@
 //   P = exp2(s - m)      one thread per row: cap, bias and mask of its row, running maximum m that is
 //                        raised (with a rescale of O in TMEM) only when it grows by more than 2^8,
 //                        P as bf16 over its S buffer. Capped scores, e^-cap to e^cap, would do without a
-//                        maximum (prompts: 57.7 instead of 61.2 us), but then large values overflow
+//                        maximum (prompts: 57.7 instead of 61.1 us), but then large values overflow
 //                        and small ones vanish
 //   O += P V_j           tcgen05.mma M=128 N=d K=64, P read from TMEM
 // Two CTAs share an SM, so one's softmax runs beside the other's products. Blocks that no row of the
@@ -17,15 +17,16 @@
 // A few queries over many keys leave most rows empty: the warps of empty rows skip the softmax, the
 // keys are split over CTAs, and the partial results are joined by a second kernel.
 //
-// Rounding P to bf16 is what the second product's operands need; the row sums are of the unrounded P.
+// Rounding P to bf16 is what the second product's operands need; the row sums are of the unrounded P. It leaves
+// outputs off by 0.0023 of their size, where an fp32 computation rounded once is off by 0.0017.
 // With rest (the output to 16 bits, for the gradients) P goes in as two bf16 terms, the second of them
 // what the rounding of the first left, behind it in the S buffer, and the second product is made twice.
 //
 // Bound by the chain of a softmax warp's step (wait, load, maximum, exponentials, store), not by the SFU
 // alone: a polynomial on the FMA pipe for 1/8 to 1/2 of the exponentials gained nothing (packed clips 160 us
 // without, 161 to 168 with). Measured, d = 128:
-// packed clips of 16380 tokens, 6 heads: 161 us, 622 TFLOP/s; prompts of 2 x 2047 tokens, 16 / 4 heads, capped:
-// 61 us; with rest, 8192 causal tokens, 12 heads: 232 us, tensor pipe 73 % active (186 us without rest).
+// packed clips of 16380 tokens, 6 heads: 158 us, 633 TFLOP/s; prompts of 2 x 2047 tokens, 16 / 4 heads, capped:
+// 61 us; with rest, 8192 causal tokens, 12 heads: 234 us, tensor pipe 72 % active (183 us without rest).
 //
 // Every wait is bounded; one that runs out stops every role without leaving a copy or product in
 // flight, is reported in the status word, and makes the tile's rows NaN.

@@ -14,8 +14,8 @@
 // takes 16 (d = 128) or 32 (d = 64) tokens and walks over heads: the cosines and sines of a
 // token are loaded once and stay in registers for all of its heads, reads of a token's heads are
 // neighbours in memory, and so are the writes of neighbouring tokens of one head. kUnroll heads
-// are in flight at a time. Measured: 32760 tokens, 40 + 40 heads of 128: 218 us, 96 % of the copy rate;
-// 8192 tokens, 12 + 12 heads: 21 us, 77 %; with gradients, 2 x 4099 tokens, 16 + 4 heads of 64: 33 us, 50 %.
+// are in flight at a time. Measured: 32760 tokens, 40 + 40 heads of 128: 217 us, 97 % of the copy rate;
+// 8192 tokens, 12 + 12 heads: 20 us, 79 %; with gradients, 2 x 4099 tokens, 16 + 4 heads of 64: 33 us, 50 %.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -448,6 +448,7 @@ typedef struct {
  *              hidden keys have to hold numbers: a NaN or an infinity among the keys that some query sees may
  *              make NaN of rows that do not see it.
  *  prefix_len  int32 [B]: with causal, keys below it are visible to every query.
+ *              prefix_len is one number per sequence, for all of its documents.
  *  doc_q, doc_k int32 [B, Sq] and [B, Sk], both or neither: a query sees only keys of an equal
  *              document number; a negative number is padding, sees nothing and is seen by nothing
  *              (padding queries, keys and output gradients may hold anything).
@@ -467,10 +468,11 @@ typedef struct {
  * A row that sees no key is written as zeros, with lse = -inf. lse: float [B, Hq, Sq] (dense), the
  * natural-log normaliser of each row, or NULL. rest: NULL, or a bf16 tensor like out (bf16 only)
  * that receives what out's rounding left over: out + rest is the result to 16 bits (the weights
- * then enter as two bf16 terms), which the gradients of short or sharply peaked rows need. Few queries over many keys (single tokens over
- * a cache) are split over the keys and joined. mask: NULL for none. workspace: 256-byte aligned,
- * fvattn_dense_attn_workspace_bytes(shape, mask) bytes (may be 0; (size_t)-1 on invalid
- * arguments; host only).
+ * then enter as two bf16 terms), which the gradients of short or sharply peaked rows need. Weighted sums are
+ * made in fp32 with weights of up to 2^8: |V| times the keys that a row sees has to stay below 2^119. Few
+ * queries over many keys (single tokens over a cache) are split over the keys and joined. mask: NULL
+ * for none. workspace: 256-byte aligned, fvattn_dense_attn_workspace_bytes(shape, mask) bytes (may be
+ * 0; (size_t)-1 on invalid arguments; host only).
  *
  * fvattn_dense_attn_bwd -- gradients of out with respect to q, k and v for the output gradient
  * dout, from the forward call's out, rest (or NULL) and lse (required). Shared key heads receive the sum
