@@ -418,21 +418,30 @@ class LazyRouter:
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, step: int, *,
                  out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        if stream is not None:
+            if stream.device != q.device:
+                raise ValueError(f"the stream is on {stream.device}, q on {q.device}")
+            # what the step makes comes from that stream's memory (around.py says why)
+            with torch.cuda.stream(stream):
+                o = self(q, k, v, step, out=out)
+            if out is None:
+                o.record_stream(torch.cuda.current_stream(q.device))
+            return o
         if step < self.dense_steps or (self.last_step is not None and step < self.last_step):
             self.last_refresh = None           # another generation's routing
         self.last_step = step
         if step < self.dense_steps:
-            return dense_attn(q, k, v, out=out, stream=stream)
+            return dense_attn(q, k, v, out=out)
         if self.should_refresh(step, q.shape):
             B, H, S, _ = q.shape
             if self.csr is None or (self.csr.B, self.csr.H, self.csr.S) != (B, H, S):
                 self.csr = alloc_csr(B, H, S, q.device, codes=self.cfg.frame_exact)
                 self.workspace = None
-            route(q, k, self.cfg, csr=self.csr, workspace=self.workspace, stream=stream)
+            route(q, k, self.cfg, csr=self.csr, workspace=self.workspace)
             self.workspace = self.csr._workspace
             self.last_refresh = step
             self.routed += 1
-        return sparse_attn(q, k, v, self.csr, out=out, stream=stream)
+        return sparse_attn(q, k, v, self.csr, out=out)
 
     def from_projections(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, step: int,
                          q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
